@@ -495,3 +495,116 @@ extern "C" int iqk_gemv_static(const iqk_weights* w, int32_t expert, const float
   return from_launch(
       launch_gemv(wd, w->fmt, expert, V, x, T, y, static_cast<char*>(scratch), (cudaStream_t)stream, sms, false));
 }
+
+// ------------------------------------------------------------------ routing
+extern "C" int iqk_moe_topk(const void* logits, int32_t dtype, int64_t row_stride, int32_t T, int32_t experts,
+                            int32_t topk, int32_t score, const float* bias, int32_t groups, int32_t topk_groups,
+                            int32_t group_top, int32_t renorm, float scale, int32_t* ids, float* p, void* stream) {
+  if (dtype != IQK_F32 && dtype != IQK_BF16) return IQK_EINVAL;
+  if (score != IQK_SOFTMAX && score != IQK_SIGMOID) return IQK_EINVAL;
+  if (T < 0 || experts < 1 || topk < 1 || groups < 1 || topk_groups < 1 || topk_groups > groups) return IQK_EINVAL;
+  if (experts % groups || (group_top != 1 && group_top != 2)) return IQK_EINVAL;
+  if (topk > topk_groups * (experts / groups)) return IQK_EINVAL;  // topk_groups <= groups: at most `experts`
+  if (experts > kTopkMaxExperts || topk > 16 || groups > kTopkMaxGroups) return IQK_EUNSUPPORTED;
+  if (T == 0) return IQK_OK;
+  if (!logits || !ids || !p || !aligned(logits, dtype == IQK_F32 ? 4 : 2) || !aligned(bias, 4) || !aligned(ids, 4) ||
+      !aligned(p, 4))
+    return IQK_EINVAL;
+  if (T > 1 && row_stride < experts) return IQK_EINVAL;
+  TopkArgs a = {};
+  a.logits = logits;
+  a.bias = bias;
+  a.ids = ids;
+  a.p = p;
+  a.stride = T > 1 ? row_stride : 0;
+  a.T = T;
+  a.experts = experts;
+  a.topk = topk;
+  a.groups = groups;
+  a.topk_groups = topk_groups;
+  a.group_top = group_top;
+  a.scale = scale;
+  a.sigmoid = score == IQK_SIGMOID;
+  a.renorm = renorm != 0;
+  return from_launch(launch_topk(a, dtype == IQK_BF16, (cudaStream_t)stream));
+}
+
+// ------------------------------------------------- 8-bit block-scaled products
+extern "C" int iqk_fp8_quantize(const uint16_t* x, int64_t row_stride, int32_t T, int32_t cols, uint8_t* q, float* s,
+                                void* stream) {
+  if (T < 0) return IQK_EINVAL;
+  if (cols < 16 || cols % 16) return IQK_ESHAPE;
+  if (T == 0) return IQK_OK;
+  if (!x || !q || !s || !aligned(x, 16) || !aligned(q, 16) || !aligned(s, 4)) return IQK_EINVAL;
+  if (T > 1 && (row_stride < cols || row_stride % 8)) return IQK_EINVAL;
+  if ((int64_t)T * fp8_blocks(cols) > (int64_t)1 << 30) return IQK_EUNSUPPORTED;
+  const int sms = num_sms();
+  if (sms < 0) return cuda_fail(cudaGetLastError());
+  return from_launch(launch_fp8_quantize(x, T > 1 ? row_stride : 0, T, cols, q, s, (cudaStream_t)stream, sms));
+}
+
+namespace {
+int check_fp8(const uint8_t* wq, const float* ws) {
+  return wq && ws && aligned(wq, 16) && aligned(ws, 4) ? IQK_OK : IQK_EINVAL;
+}
+constexpr int kFp8MaxT = 65536;
+}  // namespace
+
+extern "C" int iqk_fp8_linear(const uint8_t* wq, const float* ws, int32_t rows, int32_t cols, const uint8_t* xq,
+                              const float* xs, int32_t T, const void* add, void* y, int32_t y_dtype, void* stream) {
+  if (T < 0 || (y_dtype != IQK_F32 && y_dtype != IQK_BF16)) return IQK_EINVAL;
+  if (rows < 1 || cols < 16 || cols % 16) return IQK_ESHAPE;
+  if (T > kFp8MaxT) return IQK_EUNSUPPORTED;
+  int rc;
+  if ((rc = check_fp8(wq, ws))) return rc;
+  if (T == 0) return IQK_OK;
+  const size_t item = y_dtype == IQK_F32 ? 4 : 2;
+  if ((rc = check_fp8(xq, xs)) || !y || !aligned(y, item) || !aligned(add, item)) return IQK_EINVAL;
+  const int sms = num_sms();
+  if (sms < 0) return cuda_fail(cudaGetLastError());
+  Fp8Args a = {};
+  a.w0 = {wq, ws};
+  a.w1 = a.w0;
+  a.xq = xq;
+  a.xs = xs;
+  a.add = add;
+  a.y = y;
+  a.T = T;
+  a.rows = rows;
+  a.cols = cols;
+  a.nkb = fp8_blocks(cols);
+  a.f32 = y_dtype == IQK_F32;
+  return from_launch(launch_fp8_product(a, false, (cudaStream_t)stream, sms));
+}
+
+extern "C" int iqk_fp8_gate_up(const uint8_t* gate_q, const float* gate_s, const uint8_t* up_q, const float* up_s,
+                               int32_t inter, int32_t cols, const uint8_t* xq, const float* xs, int32_t T, uint8_t* hq,
+                               float* hs, void* stream) {
+  if (T < 0) return IQK_EINVAL;
+  if (inter < 16 || inter % 16 || cols < 16 || cols % 16) return IQK_ESHAPE;
+  if (T > kFp8MaxT) return IQK_EUNSUPPORTED;
+  int rc;
+  if ((rc = check_fp8(gate_q, gate_s)) || (rc = check_fp8(up_q, up_s))) return rc;
+  if (T == 0) return IQK_OK;
+  if ((rc = check_fp8(xq, xs)) || (rc = check_fp8(hq, hs))) return rc;
+  const int sms = num_sms();
+  if (sms < 0) return cuda_fail(cudaGetLastError());
+  Fp8Args a = {};
+  a.w0 = {gate_q, gate_s};
+  a.w1 = {up_q, up_s};
+  a.xq = xq;
+  a.xs = xs;
+  a.y = hq;
+  a.hs = hs;
+  a.T = T;
+  a.rows = inter;
+  a.cols = cols;
+  a.nkb = fp8_blocks(cols);
+  return from_launch(launch_fp8_product(a, true, (cudaStream_t)stream, sms));
+}
+
+extern "C" int iqk_fp8_status(void* stream) {
+  int32_t s = 0;
+  if (read_fp8_status((cudaStream_t)stream, &s)) return cuda_fail(cudaGetLastError());
+  return s ? IQK_ETIMEOUT : IQK_OK;
+}

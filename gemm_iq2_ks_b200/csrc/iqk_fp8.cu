@@ -1,0 +1,654 @@
+// 8-bit floating point (e4m3) with block scales: quantisation of activations,
+// the product of two quantised operands, and the gate/up step of a dense
+// expert (two products, SwiGLU, quantisation of the result).
+//
+// An activation row has one float32 scale per 128 columns, a weight matrix one
+// per 128 x 128 block, so a product is
+//   y[t][o] = sum_b xs[t][b] ws[o / 128][b] sum_{k in block b} xq[t][k] wq[o][k].
+// The inner sums run on the tensor cores with float32 accumulators; the scales
+// are applied to each 128-column block's sum in float32 on the way into the
+// register accumulators.
+#include <algorithm>
+
+#include "iqk_device.cuh"
+#include "iqk_internal.h"
+#include "iqk_tc.cuh"
+
+namespace iqk {
+
+namespace {
+
+__device__ int32_t g_fp8_status;  // nonzero once a bounded wait of a product expired
+
+constexpr float kE4m3Max = 448.0f;
+constexpr float kAmaxMin = 0x1p-100f;  // a group's largest magnitude counts as at least this
+
+// Two e4m3 codes, nearest even, saturating.
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  return e4m3x2(a, b) | (e4m3x2(c, d) << 16);
+}
+
+// ------------------------------------------------------------- quantisation
+//
+// q = e4m3(448 x / m) with m the group's largest magnitude, exactly: the
+// quotient of two bfloat16 numbers times 448 = 7 * 64 is either a rounding
+// border of e4m3 (a number of at most 5 significant bits) or at least 2^-13
+// of it away, because the difference 7 X 2^a - M B 2^b of integers with
+// X, M < 2^8 and B < 2^5 is not zero and one of a, b is. x * (448 / m) in
+// float32 is within 2^-23 of the quotient; rounding that to 18 significant
+// bits (a step of at most 2^-17) returns a border exactly and keeps every
+// other quotient on its side. This costs two integer operations instead of a
+// division for each element.
+__device__ __forceinline__ float snap18(float t) {
+  return __uint_as_float((__float_as_uint(t) + 0x20u) & ~0x3fu);
+}
+
+constexpr int kQuantThreads = 256;
+constexpr int kQuantUnroll = 4;
+
+// 16 lanes take one group of 128 columns, 8 columns (16 bytes) each.
+__global__ void __launch_bounds__(kQuantThreads) k_fp8_quantize(const uint16_t* x, int64_t stride, int cols,
+                                                                int nkb, FastDiv by_nkb, int items,
+                                                                uint8_t* q, float* s) {
+  griddep_wait();
+  const int sub = threadIdx.x & 15;
+  const int per = gridDim.x * (kQuantThreads / 16);
+  for (int it0 = blockIdx.x * (kQuantThreads / 16) + (threadIdx.x >> 4); it0 < items; it0 += per * kQuantUnroll) {
+    uint4 v[kQuantUnroll];
+    int row[kQuantUnroll], col[kQuantUnroll];
+#pragma unroll
+    for (int u = 0; u < kQuantUnroll; u++) {
+      const int it = it0 + u * per;
+      row[u] = (int)by_nkb.div((uint32_t)it);
+      col[u] = (it - row[u] * nkb) * kFp8Block + sub * 8;
+      v[u] = make_uint4(0, 0, 0, 0);
+      if (it < items && col[u] < cols) v[u] = ld_u4(x + row[u] * stride + col[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < kQuantUnroll; u++) {
+      const int it = it0 + u * per;
+      const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+      uint32_t m2 = 0;
+#pragma unroll
+      for (int j = 0; j < 4; j++) m2 = __vmaxu2(m2, w[j] & 0x7fff7fffu);
+#pragma unroll
+      for (int d = 8; d; d >>= 1) m2 = __vmaxu2(m2, __shfl_xor_sync(0xffffffffu, m2, d));
+      const uint32_t mb = (m2 & 0xffffu) > (m2 >> 16) ? (m2 & 0xffffu) : (m2 >> 16);
+      const bool fine = mb < 0x7f80u;
+      const float most = fmaxf(__uint_as_float(mb << 16), kAmaxMin);
+      const float inv = fine ? kE4m3Max / most : 0.f;
+      float t[8];
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        t[2 * j] = snap18(__uint_as_float(w[j] << 16) * inv);
+        t[2 * j + 1] = snap18(__uint_as_float(w[j] & 0xffff0000u) * inv);
+      }
+      uint2 o;
+      o.x = e4m3x4(t[0], t[1], t[2], t[3]);
+      o.y = e4m3x4(t[4], t[5], t[6], t[7]);
+      if (!fine) o = make_uint2(0, 0);
+      if (it < items && col[u] < cols) {
+        *reinterpret_cast<uint2*>(q + (int64_t)row[u] * cols + col[u]) = o;
+        if (sub == 0) s[it] = fine ? most / kE4m3Max : __int_as_float(0x7fffffff);
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------ few tokens
+//
+// Up to 16 tokens: a stream over the weights. A CTA takes 16 rows (16 gate and
+// 16 up rows), its warps the 128-column blocks in turn; each lane loads the
+// 16-byte pieces of its fragments straight from global memory (the k order
+// inside a 64-column chunk is the same permutation for both operands, so the
+// dot products are unchanged), all blocks of a round before the first use.
+
+__device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ uint32_t peer_smem(const void* p, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void st_peer(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+__device__ __forceinline__ float4 ld_peer4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+// Output element of the plain product.
+__device__ __forceinline__ void put_y(const Fp8Args& A, int64_t i, float v) {
+  if (A.f32) {
+    if (A.add) v += static_cast<const float*>(A.add)[i];
+    static_cast<float*>(A.y)[i] = v;
+  } else {
+    if (A.add) v += bf16_bits_to_f32(static_cast<const uint16_t*>(A.add)[i]);
+    static_cast<uint16_t*>(A.y)[i] = f32_to_bf16_bits(v);
+  }
+}
+
+__device__ __forceinline__ float magnitude(float h) {  // infinity for what is not finite
+  const float m = fabsf(h);
+  return m <= 3.402823466e38f ? m : __int_as_float(0x7f800000);
+}
+
+constexpr int kGemvMaxT = 16;
+constexpr int kGemvRows = 16;
+constexpr int kGemvWarps(bool gu) { return gu ? 16 : 8; }  // at most
+constexpr int kGuCluster = kFp8Block / kGemvRows;  // CTAs whose rows make up one scale's 128 columns of h
+
+template <int NT, bool GU, int U>
+__global__ void __launch_bounds__(kGemvWarps(GU) * 32) k_fp8_gemv(const __grid_constant__ Fp8Args A) {
+  constexpr int M = GU ? 2 : 1;
+  extern __shared__ __align__(16) float gemv_smem[];  // [warps][M][8 NT tokens][16 rows]
+  __shared__ float s_amax[kGuCluster][kGemvMaxT];
+  griddep_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+  const int g = lane >> 2, tq = lane & 3;
+  const int row0 = blockIdx.x * kGemvRows;
+  if (GU) cluster_arrive();  // every CTA of the cluster runs before its shared memory is written to
+  float acc[M][NT][4] = {};
+  for (int kb0 = warp; kb0 < A.nkb; kb0 += nw * U) {
+    uint4 w[U][M][2][2], x[U][NT][2];  // weights: [row g, g + 8][64-column chunk]; x: [token g][chunk]
+    float sw[U][M], sx[U][NT][2];
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+      const int kb = kb0 + u * nw;
+      const bool in = kb < A.nkb;
+#pragma unroll
+      for (int m = 0; m < M; m++) {
+        const Fp8Mat& W = m ? A.w1 : A.w0;
+#pragma unroll
+        for (int r = 0; r < 2; r++)
+#pragma unroll
+          for (int c = 0; c < 2; c++) {
+            const int row = row0 + g + 8 * r, k = kb * kFp8Block + 64 * c + 16 * tq;
+            w[u][m][r][c] = make_uint4(0, 0, 0, 0);
+            if (in && row < A.rows && k < A.cols)
+              w[u][m][r][c] = ld_u4(W.q + (int64_t)row * A.cols + k);
+          }
+        sw[u][m] = in && row0 < A.rows ? W.s[(int64_t)(row0 / kFp8Block) * A.nkb + kb] : 0.f;
+      }
+#pragma unroll
+      for (int n = 0; n < NT; n++) {
+#pragma unroll
+        for (int c = 0; c < 2; c++) {
+          const int tok = 8 * n + g, k = kb * kFp8Block + 64 * c + 16 * tq;
+          x[u][n][c] = make_uint4(0, 0, 0, 0);
+          if (in && tok < A.T && k < A.cols)
+            x[u][n][c] = ld_u4(A.xq + (int64_t)tok * A.cols + k);
+        }
+#pragma unroll
+        for (int j = 0; j < 2; j++) {
+          const int tok = 8 * n + 2 * tq + j;
+          sx[u][n][j] = in && tok < A.T ? A.xs[(int64_t)tok * A.nkb + kb] : 0.f;
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+      if (kb0 + u * nw >= A.nkb) break;
+#pragma unroll
+      for (int m = 0; m < M; m++)
+#pragma unroll
+        for (int n = 0; n < NT; n++) {
+          float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int c = 0; c < 2; c++) {
+            const uint4 a = w[u][m][0][c], b = w[u][m][1][c], v = x[u][n][c];
+            mma_e4m3(d, a.x, b.x, a.y, b.y, v.x, v.y);
+            mma_e4m3(d, a.z, b.z, a.w, b.w, v.z, v.w);
+          }
+          // d: (row g, tokens 2 tq, 2 tq + 1), (row g + 8, the same)
+          const float s0 = sw[u][m] * sx[u][n][0], s1 = sw[u][m] * sx[u][n][1];
+          acc[m][n][0] += d[0] * s0;
+          acc[m][n][1] += d[1] * s1;
+          acc[m][n][2] += d[2] * s0;
+          acc[m][n][3] += d[3] * s1;
+        }
+    }
+  }
+  constexpr int TOK = 8 * NT;
+#pragma unroll
+  for (int m = 0; m < M; m++)
+#pragma unroll
+    for (int n = 0; n < NT; n++)
+#pragma unroll
+      for (int j = 0; j < 4; j++)
+        gemv_smem[((warp * M + m) * TOK + 8 * n + 2 * tq + (j & 1)) * kGemvRows + g + 8 * (j >> 1)] = acc[m][n][j];
+  __syncthreads();
+  // Warps' sums in order; 16 consecutive lanes hold one token's 16 rows.
+  if (!GU) {
+    for (int i = threadIdx.x; i < A.T * kGemvRows; i += blockDim.x) {
+      float v = 0.f;
+      for (int k = 0; k < nw; k++) v += gemv_smem[k * TOK * kGemvRows + i];
+      const int tok = i / kGemvRows, row = row0 + i % kGemvRows;
+      if (row < A.rows) put_y(A, (int64_t)tok * A.rows + row, v);
+    }
+    return;
+  }
+  float* hbuf = gemv_smem + (size_t)nw * M * TOK * kGemvRows;  // [tokens][16]
+  const uint32_t rank = cluster_rank();
+  cluster_wait();
+  for (int i = threadIdx.x; i < TOK * kGemvRows; i += blockDim.x) {  // whole half-warps
+    float gv = 0.f, uv = 0.f;
+    for (int k = 0; k < nw; k++) {
+      gv += gemv_smem[(k * M) * TOK * kGemvRows + i];
+      uv += gemv_smem[(k * M + M - 1) * TOK * kGemvRows + i];
+    }
+    const float h = silu_f32(gv) * uv;
+    hbuf[i] = h;
+    float m = row0 + i % kGemvRows < A.rows ? magnitude(h) : 0.f;
+#pragma unroll
+    for (int d = 8; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    if (i % kGemvRows < kGuCluster) st_peer(peer_smem(&s_amax[rank][i / kGemvRows], i % kGemvRows), m);
+  }
+  cluster_arrive();
+  cluster_wait();
+  if (row0 >= A.rows) return;
+  for (int i = threadIdx.x; i < A.T * 4; i += blockDim.x) {  // four rows of one token each
+    const int tok = i / 4, r = 4 * (i % 4);
+    float most = 0.f;
+#pragma unroll
+    for (int k = 0; k < kGuCluster; k++) most = fmaxf(most, s_amax[k][tok]);
+    const bool fine = most <= 3.402823466e38f;
+    most = fmaxf(most, kAmaxMin);
+    const float inv = fine ? kE4m3Max / most : 0.f;
+    const float4 h = *reinterpret_cast<const float4*>(hbuf + tok * kGemvRows + r);
+    const uint32_t o = fine ? e4m3x4(h.x * inv, h.y * inv, h.z * inv, h.w * inv) : 0u;
+    *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(A.y) + (int64_t)tok * A.rows + row0 + r) = o;
+    if (rank == 0 && r == 0)
+      A.hs[(int64_t)tok * ((A.rows + kFp8Block - 1) / kFp8Block) + row0 / kFp8Block] =
+          fine ? most / kE4m3Max : __int_as_float(0x7fffffff);
+  }
+}
+
+// ----------------------------------------------------------- many tokens
+//
+// tcgen05 tiles of 128 tokens x BN weight rows (gate_up: 128 gate and 128 up
+// rows side by side). One 128-column block is one pipeline step: TMA brings
+// both operands' 128-byte rows (128-byte swizzle), four MMAs leave the block's
+// sums in one of the tensor-memory buffers, and two warpgroups add them, times
+// the two scales, to float32 accumulators in registers (thread = token row;
+// each warpgroup half of the columns). With few tiles the CTAs of a cluster
+// split the blocks and add their accumulators over distributed shared memory,
+// in rank order.
+constexpr int kBM = 128;
+constexpr int kEpiWarps = 8, kTmaWarp = 8, kMmaWarp = 9;
+constexpr int kGemmThreads = 10 * 32;
+constexpr int kGemmStageBytes(int BN) { return (kBM + BN) * kFp8Block; }
+constexpr int kGemmStages(int BN) { return BN == 256 ? 4 : 6; }
+constexpr int kPitch(int BN) { return BN + 4; }  // floats between rows of the shared accumulators
+constexpr size_t kGemmSmem(int BN) {
+  const size_t a = (size_t)kGemmStages(BN) * kGemmStageBytes(BN), b = (size_t)kBM * kPitch(BN) * 4;
+  return (a > b ? a : b) + 256 + 1024;
+}
+
+__device__ __forceinline__ bool gemm_wait(uint64_t* bar, uint32_t par, volatile uint32_t* abort_flag) {
+  for (uint32_t i = 0; i < (1u << 24); i++) {
+    if (mbar_try_wait(bar, par)) return true;
+    if ((i & 1023u) == 1023u && *abort_flag) return false;
+  }
+  *abort_flag = 1;
+  atomicOr(&g_fp8_status, 2);
+  return false;
+}
+
+__device__ __forceinline__ void mma_ss_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+// The wait names the loaded registers, so that nothing reads them ahead of it.
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                   "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                   "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
+                   "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                   "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+
+// Instruction descriptor, kind::f8f6f4: e4m3 A and B (format code 0), float32
+// accumulator, both K-major, M = 128, N = n.
+__host__ __device__ constexpr uint32_t idesc_e4m3_m128(uint32_t n) {
+  return (1u << 4) | ((n >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+template <int BN, bool GU>
+__global__ void __launch_bounds__(kGemmThreads, 1)
+    k_fp8_gemm(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap m0,
+               const __grid_constant__ CUtensorMap m1, const __grid_constant__ Fp8Args A, int tiles_m, int split) {
+  constexpr int ST = kGemmStages(BN), SB = kGemmStageBytes(BN), NBUF = 512 / BN, NC = BN / 2;
+  constexpr int NB = GU ? 128 : BN;  // output columns of a tile
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kGemmSmem(BN) - 256 - 1024);
+  uint64_t* empty = full + ST;
+  uint64_t* tfull = empty + ST;
+  uint64_t* tfree = tfull + NBUF;
+  uint64_t* drain = tfree + NBUF;
+  uint32_t* holder = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile uint32_t* abort_flag = holder + 1;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = split > 1 ? (int)cluster_rank() : 0;
+  const int tile = blockIdx.x / split;
+  const int t0 = (tile % tiles_m) * kBM, n0 = (tile / tiles_m) * NB;
+  const int kb_lo = (int)((int64_t)A.nkb * rank / split), kb_hi = (int)((int64_t)A.nkb * (rank + 1) / split);
+  const int steps = kb_hi - kb_lo;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < ST; i++) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < NBUF; i++) {
+      mbar_init(&tfull[i], 1);
+      mbar_init(&tfree[i], kEpiWarps);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kTmaWarp && lane == 0) {
+    prefetch_tensormap(&mx);
+    prefetch_tensormap(&m0);
+    prefetch_tensormap(&m1);
+  }
+  if (warp == kMmaWarp) tmem_alloc(holder, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *holder;
+  griddep_wait();
+
+  if (warp == kTmaWarp) {
+    if (lane == 0) {
+      int i = 0;
+      for (; i < steps; i++) {
+        const int s = i % ST, k = (kb_lo + i) * kFp8Block;
+        if (!gemm_wait(&empty[s], ((i / ST) & 1) ^ 1, abort_flag)) break;
+        uint8_t* a = smem + s * SB;
+        mbar_arrive_expect_tx(&full[s], SB);
+        tma_load_2d(a, &mx, k, t0, &full[s]);
+        tma_load_2d(a + kBM * kFp8Block, &m0, k, n0, &full[s]);
+        if (BN == 256) tma_load_2d(a + (kBM + 128) * kFp8Block, &m1, k, GU ? n0 : n0 + 128, &full[s]);
+      }
+      if (i < steps)  // a wait expired: let the copies in flight land
+        for (int j = i < ST ? 0 : i - ST; j < i; j++) mbar_wait_bounded(&full[j % ST], (j / ST) & 1);
+    }
+  } else if (warp == kMmaWarp) {
+    if (lane == 0) {
+      int i = 0;
+      for (; i < steps; i++) {
+        const int s = i % ST, b = i % NBUF;
+        if (!gemm_wait(&full[s], (i / ST) & 1, abort_flag)) break;
+        if (!gemm_wait(&tfree[b], ((i / NBUF) & 1) ^ 1, abort_flag)) break;
+        tc_fence_after();
+        const uint32_t a = smem_u32(smem + s * SB);
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+          mma_ss_e4m3(tmem + b * BN, sdesc_kmajor_sw128(a + 32u * j),
+                      sdesc_kmajor_sw128(a + kBM * kFp8Block + 32u * j), idesc_e4m3_m128(BN), j != 0);
+        tc_commit(&empty[s]);
+        tc_commit(&tfull[b]);
+      }
+      if (i < steps) {  // a wait expired: let the products in flight end before their tensor memory is given back
+        tc_commit(drain);
+        mbar_wait_bounded(drain, 0);
+      }
+    }
+  } else {
+    const int half = warp >> 2, q = warp & 3;
+    const int t = t0 + 32 * q + lane;
+    const bool rows_in = t0 + 32 * q < A.T;  // some row of this warp exists
+    const Fp8Mat& W = GU && half ? A.w1 : A.w0;
+    // the weight block of this warpgroup's columns (past the last: any, its columns are not stored)
+    const int wb = min((n0 + (GU || BN == 128 ? 0 : 128 * half)) / kFp8Block, (A.rows - 1) / kFp8Block);
+    const float* ws = W.s + (int64_t)wb * A.nkb + kb_lo;
+    const float* xs = A.xs + (int64_t)min(t, A.T - 1) * A.nkb + kb_lo;
+    float acc[NC];
+#pragma unroll
+    for (int c = 0; c < NC; c++) acc[c] = 0.f;
+    bool ok = true;
+    float sc = steps > 0 ? ws[0] * xs[0] : 0.f;
+    for (int i = 0; i < steps && ok; i++) {
+      const int b = i % NBUF;
+      const float sn = i + 1 < steps ? ws[i + 1] * xs[i + 1] : 0.f;
+      ok = gemm_wait(&tfull[b], (i / NBUF) & 1, abort_flag);
+      tc_fence_after();
+      if (rows_in) {
+        const uint32_t base = tmem + ((uint32_t)(32 * q) << 16) + b * BN + half * NC;
+#pragma unroll
+        for (int c0 = 0; c0 < NC; c0 += 32) {
+          uint32_t r[32];
+          tmem_ld32(base + c0, r);
+          tmem_wait_ld(r);
+#pragma unroll
+          for (int c = 0; c < 32; c++) acc[c0 + c] += __uint_as_float(r[c]) * sc;
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&tfree[b]);
+      sc = sn;
+    }
+    // All MMAs have read their operands: the stages take the accumulators.
+    if (rows_in && ok) {
+      float* dst = reinterpret_cast<float*>(smem) + (size_t)(32 * q + lane) * kPitch(BN) + half * NC;
+#pragma unroll
+      for (int c = 0; c < NC; c += 4)
+        *reinterpret_cast<float4*>(dst + c) = make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+  if (split > 1) {
+    cluster_arrive();
+    cluster_wait();
+  }
+  // One warp per row, rows dealt to the cluster's CTAs and their warps in turn.
+  const int nrow = min(kBM, A.T - t0);
+  const int hblocks = (A.rows + kFp8Block - 1) / kFp8Block;
+  for (int r = rank + split * warp; r < nrow; r += split * (kGemmThreads / 32)) {
+    float4 v[BN / 128];
+#pragma unroll
+    for (int h = 0; h < BN / 128; h++) {
+      const float* src = reinterpret_cast<const float*>(smem) + (size_t)r * kPitch(BN) + 128 * h + 4 * lane;
+      if (split == 1) {
+        v[h] = *reinterpret_cast<const float4*>(src);
+      } else {
+        v[h] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = 0; k < split; k++) {
+          const float4 o = ld_peer4(peer_smem(src, k));
+          v[h].x += o.x;
+          v[h].y += o.y;
+          v[h].z += o.z;
+          v[h].w += o.w;
+        }
+      }
+    }
+    const int64_t t = t0 + r;
+    if (GU) {
+      const float4 gv = v[0], uv = v[BN / 128 - 1];
+      const int n = n0 + 4 * lane;  // rows is a multiple of 16: all four columns exist or none
+      const float h0 = silu_f32(gv.x) * uv.x, h1 = silu_f32(gv.y) * uv.y, h2 = silu_f32(gv.z) * uv.z,
+                  h3 = silu_f32(gv.w) * uv.w;
+      float most =
+          n < A.rows ? fmaxf(fmaxf(magnitude(h0), magnitude(h1)), fmaxf(magnitude(h2), magnitude(h3))) : 0.f;
+#pragma unroll
+      for (int d = 16; d; d >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
+      const bool fine = most <= 3.402823466e38f;
+      most = fmaxf(most, kAmaxMin);
+      const float inv = fine ? kE4m3Max / most : 0.f;
+      const uint32_t o = fine ? e4m3x4(h0 * inv, h1 * inv, h2 * inv, h3 * inv) : 0u;
+      if (n < A.rows) *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(A.y) + t * A.rows + n) = o;
+      if (lane == 0) A.hs[t * hblocks + n0 / kFp8Block] = fine ? most / kE4m3Max : __int_as_float(0x7fffffff);
+    } else {
+#pragma unroll
+      for (int h = 0; h < BN / 128; h++) {
+        const int n = n0 + 128 * h + 4 * lane;
+        const float w[4] = {v[h].x, v[h].y, v[h].z, v[h].w};
+#pragma unroll
+        for (int c = 0; c < 4; c++)
+          if (n + c < A.rows) put_y(A, t * A.rows + n + c, w[c]);
+      }
+    }
+  }
+  if (split > 1) {  // the peers have read this CTA's accumulators
+    cluster_arrive();
+    cluster_wait();
+  }
+}
+
+cudaLaunchAttribute pdl() {
+  cudaLaunchAttribute a = {};
+  a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a.val.programmaticStreamSerializationAllowed = 1;
+  return a;
+}
+cudaLaunchAttribute cluster_of(int n) {
+  cudaLaunchAttribute a = {};
+  a.id = cudaLaunchAttributeClusterDimension;
+  a.val.clusterDim.x = (unsigned)n;
+  a.val.clusterDim.y = 1;
+  a.val.clusterDim.z = 1;
+  return a;
+}
+
+template <int NT, bool GU, int U>
+int launch_gemv_nt(const Fp8Args& a, cudaStream_t st) {
+  const int nw = std::min(kGemvWarps(GU), (a.nkb + U - 1) / U);
+  const int tiles = (a.rows + kGemvRows - 1) / kGemvRows;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(GU ? (tiles + kGuCluster - 1) / kGuCluster * kGuCluster : tiles));
+  cfg.blockDim = dim3((unsigned)nw * 32);
+  cfg.dynamicSmemBytes = (size_t)(nw * (GU ? 2 : 1) + (GU ? 1 : 0)) * 8 * NT * kGemvRows * 4;
+  cfg.stream = st;
+  cudaLaunchAttribute at[2] = {pdl(), cluster_of(kGuCluster)};
+  cfg.attrs = at;
+  cfg.numAttrs = GU ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, k_fp8_gemv<NT, GU, U>, a) == cudaSuccess ? 0 : -4;
+}
+
+// Map of a row-major e4m3 matrix, boxes of 128 rows x 128 columns; columns and rows past the end read as zero.
+int make_e4m3_map(CUtensorMap* map, const uint8_t* base, int rows, int cols) {
+  EncodeTiledFn enc = encode_tiled_fn();
+  if (!enc) return -4;
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)cols};
+  const cuuint32_t box[2] = {(cuuint32_t)kFp8Block, 128};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(base), dims, strides, box, estr,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? 0 : -4;
+}
+
+template <int BN, bool GU>
+int launch_gemm(const Fp8Args& a, int num_sms, cudaStream_t st) {
+  const int tiles_m = (a.T + kBM - 1) / kBM, nb = GU ? 128 : BN, tiles_n = (a.rows + nb - 1) / nb;
+  const int64_t tiles = (int64_t)tiles_m * tiles_n;
+  if (tiles > 0x0fffffff) return -3;
+  int split = 1;
+  while (split < 8 && tiles * split * 2 <= num_sms && split * 2 <= a.nkb) split *= 2;
+  CUtensorMap mx, m0, m1;
+  if (make_e4m3_map(&mx, a.xq, a.T, a.cols) || make_e4m3_map(&m0, a.w0.q, a.rows, a.cols) ||
+      make_e4m3_map(&m1, GU ? a.w1.q : a.w0.q, a.rows, a.cols))
+    return -4;
+  auto kern = k_fp8_gemm<BN, GU>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGemmSmem(BN)) != cudaSuccess)
+    return -4;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(tiles * split));
+  cfg.blockDim = dim3(kGemmThreads);
+  cfg.dynamicSmemBytes = kGemmSmem(BN);
+  cfg.stream = st;
+  cudaLaunchAttribute at[2] = {pdl(), cluster_of(split)};
+  cfg.attrs = at;
+  cfg.numAttrs = split > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, mx, m0, m1, a, tiles_m, split) == cudaSuccess ? 0 : -4;
+}
+
+}  // namespace
+
+int launch_fp8_quantize(const uint16_t* x, int64_t stride, int T, int cols, uint8_t* q, float* s, cudaStream_t st,
+                        int num_sms) {
+  const int nkb = fp8_blocks(cols), items = T * nkb;
+  const int per = kQuantThreads / 16;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)std::min((items + per - 1) / per, num_sms * 8));
+  cfg.blockDim = dim3(kQuantThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1] = {pdl()};
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_fp8_quantize, x, stride, cols, nkb, FastDiv::of((uint32_t)nkb), items, q, s) ==
+                 cudaSuccess
+             ? 0
+             : -4;
+}
+
+int launch_fp8_product(const Fp8Args& a, bool gate_up, cudaStream_t st, int num_sms) {
+  if (a.T <= kGemvMaxT) {
+    if (gate_up) return a.T <= 8 ? launch_gemv_nt<1, true, 2>(a, st) : launch_gemv_nt<2, true, 1>(a, st);
+    return a.T <= 8 ? launch_gemv_nt<1, false, 4>(a, st) : launch_gemv_nt<2, false, 2>(a, st);
+  }
+  if (gate_up) return launch_gemm<256, true>(a, num_sms, st);
+  const int64_t tiles = (int64_t)((a.T + kBM - 1) / kBM) * ((a.rows + 255) / 256);
+  return tiles >= num_sms ? launch_gemm<256, false>(a, num_sms, st) : launch_gemm<128, false>(a, num_sms, st);
+}
+
+int read_fp8_status(cudaStream_t st, int32_t* out) {
+  if (cudaStreamSynchronize(st) != cudaSuccess) return -4;
+  if (cudaMemcpyFromSymbol(out, g_fp8_status, 4) != cudaSuccess) return -4;
+  const int32_t zero = 0;
+  if (*out && cudaMemcpyToSymbol(g_fp8_status, &zero, 4) != cudaSuccess) return -4;
+  return 0;
+}
+
+}  // namespace iqk

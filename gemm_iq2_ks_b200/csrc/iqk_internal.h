@@ -149,6 +149,46 @@ int launch_pf_a_tile(const WDev& w, int fmt, int expert, int row0, int nrows, co
 int launch_combine(const float* rows, const float* p, int T, int topk, int H, uint16_t* y, cudaStream_t st,
                    int num_sms);
 
+// ----------------------------------------------------------------- routing
+constexpr int kTopkMaxExperts = 1024;  // 32 values in each lane of a warp
+constexpr int kTopkMaxGroups = 32;     // one lane at least for each group
+struct TopkArgs {
+  const void* logits;  // float32 or bf16 [T][experts], rows `stride` elements apart
+  const float* bias;   // [experts] or null
+  int32_t* ids;        // [T][topk]
+  float* p;            // [T][topk]
+  int64_t stride;
+  int32_t T, experts, topk, groups, topk_groups, group_top;
+  float scale;
+  bool sigmoid, renorm;
+  // set by launch_topk
+  int32_t group_size, lanes_per_group, smem_row;
+};
+int launch_topk(TopkArgs a, bool bf16, cudaStream_t st);
+
+// ------------------------------------------------------- 8-bit block-scaled
+constexpr int kFp8Block = 128;  // columns of an activation scale, rows and columns of a weight scale
+inline int fp8_blocks(int n) { return (n + kFp8Block - 1) / kFp8Block; }
+int launch_fp8_quantize(const uint16_t* x, int64_t stride, int T, int cols, uint8_t* q, float* s, cudaStream_t st,
+                        int num_sms);
+struct Fp8Mat {
+  const uint8_t* q;  // e4m3 [rows][cols]
+  const float* s;    // [ceil(rows / 128)][ceil(cols / 128)]
+};
+struct Fp8Args {
+  Fp8Mat w0, w1;      // w1: the up matrix of gate_up
+  const uint8_t* xq;  // e4m3 [T][cols]
+  const float* xs;    // [T][ceil(cols / 128)]
+  const void* add;    // y's type, or null
+  void* y;            // bf16 or float32 [T][rows]; gate_up: e4m3 codes
+  float* hs;          // gate_up: scales [T][ceil(rows / 128)]
+  int32_t T, rows, cols, nkb;
+  bool f32;
+};
+int launch_fp8_product(const Fp8Args& a, bool gate_up, cudaStream_t st, int num_sms);
+// Whether a bounded wait of a product expired since the last call (cleared), after syncing `st`.
+int read_fp8_status(cudaStream_t st, int32_t* out);
+
 // Driver entry point for cuTensorMapEncodeTiled (resolved once).
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,

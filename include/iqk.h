@@ -466,6 +466,97 @@ int iqk_floor_status(void* stream);
  */
 int iqk_set_wait_limit_ns(uint64_t limit_ns, int32_t expire);
 
+/* ------------------------------------------------------------------------
+ * Around the routed block: the router's choice of experts, and the layer's
+ * dense projections in 8-bit floating point (e4m3) with block scales.
+ * ------------------------------------------------------------------------ */
+
+typedef enum { IQK_F32 = 0, IQK_BF16 = 1 } iqk_dtype;
+typedef enum { IQK_SOFTMAX = 0, IQK_SIGMOID = 1 } iqk_score;
+
+/*
+ * iqk_moe_topk -- router logits to the ids and p that iqk_moe_decode,
+ * iqk_moe_prefill and iqk_switch_linear take.
+ *   logits: device float32 or bf16 (dtype) [T][experts], rows row_stride
+ *           elements apart (>= experts; ignored for T = 1)
+ *   s:      the row's scores, softmax over all experts or the sigmoid of each
+ *   bias:   device float32 [experts] or NULL; takes part in the selection only
+ *   selection value: s + bias; without a bias the logit (scores keep its order)
+ *   groups > 1: the experts form `groups` equal runs; a group's value is its
+ *           largest selection value (group_top = 1) or, with group_top = 2, the
+ *           sum of its two largest values of s (+ bias), one where only one is
+ *           not masked; the topk_groups best groups stay open (ties: lowest
+ *           index), the others' experts are never selected
+ *   ids:    device int32 [T][topk]: the open experts of largest selection value
+ *           in descending order, ties to the lowest index
+ *   p:      device float32 [T][topk]: scale * s, or with renorm != 0
+ *           scale * s / (sum of the selected s), float32 arithmetic; the ratio
+ *           is formed from the logits, so it also holds where the scores
+ *           themselves lie below float32's range
+ * A logit of -inf or NaN, or a bias of -inf or NaN, masks the expert: it comes
+ * behind every other open expert and its p is 0 (a row masked throughout gets
+ * valid ids and p = 0 everywhere). The softmax is over the logits that are not
+ * -inf or NaN, whatever the bias; logits of +inf share it.
+ * Selection values that are scores are compared as evaluated in float64.
+ * Limits: experts <= 1024, topk <= 16, groups <= 32 (IQK_EUNSUPPORTED);
+ * groups divides experts, topk <= topk_groups * experts / groups. T = 0 does
+ * nothing. ids and p must not overlap the inputs.
+ */
+int iqk_moe_topk(const void* logits, int32_t dtype, int64_t row_stride, int32_t T, int32_t experts, int32_t topk,
+                 int32_t score, const float* bias, int32_t groups, int32_t topk_groups, int32_t group_top,
+                 int32_t renorm, float scale, int32_t* ids, float* p, void* stream);
+
+/*
+ * iqk_fp8_quantize -- activations to e4m3 with one scale per row and 128
+ * columns (the last group of a row may be shorter).
+ *   x: device bf16 [T][cols], rows row_stride elements apart (>= cols, a
+ *      multiple of 8; ignored for T = 1), 16-byte aligned; cols a positive
+ *      multiple of 16
+ *   with m the largest magnitude of a group, counted as at least 2^-100:
+ *   s: device float32 [T][ceil(cols / 128)]: m / 448
+ *   q: device e4m3 [T][cols], 16-byte aligned: 448 x / m rounded to the nearest
+ *      e4m3 number (ties to even), exactly
+ * A group that holds an infinity or a NaN gets s = NaN and q = 0, so products
+ * of its row are NaN. The outputs must not overlap x.
+ */
+int iqk_fp8_quantize(const uint16_t* x, int64_t row_stride, int32_t T, int32_t cols, uint8_t* q, float* s,
+                     void* stream);
+
+/*
+ * iqk_fp8_linear -- the product of quantised activations and weights:
+ *   y[t][o] = round( add[t][o] + sum_b xs[t][b] ws[o / 128][b] sum_{k in block b} xq[t][k] wq[o][k] )
+ * over the blocks b of 128 columns.
+ *   wq: device e4m3 [rows][cols], ws: device float32 [ceil(rows / 128)][ceil(cols / 128)]
+ *   xq: device e4m3 [T][cols], xs: device float32 [T][ceil(cols / 128)], as iqk_fp8_quantize writes them
+ *   add: NULL, or device [T][rows] of y's type; may be y itself
+ *   y: device bf16 or float32 (y_dtype) [T][rows], written completely
+ * rows >= 1, cols a positive multiple of 16, T <= 65536; wq and xq 16-byte
+ * aligned. float32 accumulation, one rounding to y's type; the order of the
+ * sums depends on the sizes only, so equal calls give equal results.
+ */
+int iqk_fp8_linear(const uint8_t* wq, const float* ws, int32_t rows, int32_t cols, const uint8_t* xq, const float* xs,
+                   int32_t T, const void* add, void* y, int32_t y_dtype, void* stream);
+
+/*
+ * iqk_fp8_gate_up -- the first half of a dense expert in one call:
+ *   g, u = the products of x with gate and up (as iqk_fp8_linear, float32)
+ *   h = silu(g) * u in float32, quantised as iqk_fp8_quantize does (from the
+ *   float32 values, 448 h / m in float32 arithmetic): hq e4m3 [T][inter], hs
+ *   float32 [T][ceil(inter / 128)], the operands of the down product.
+ * gate, up: [inter][cols] each; inter and cols positive multiples of 16; hq
+ * 16-byte aligned. The outputs must not overlap the inputs.
+ */
+int iqk_fp8_gate_up(const uint8_t* gate_q, const float* gate_s, const uint8_t* up_q, const float* up_s, int32_t inter,
+                    int32_t cols, const uint8_t* xq, const float* xs, int32_t T, uint8_t* hq, float* hs, void* stream);
+
+/*
+ * iqk_fp8_status -- synchronises `stream`, then reports whether a bounded
+ * device wait of an iqk_fp8_linear or iqk_fp8_gate_up call expired on the
+ * current device since the last iqk_fp8_status (IQK_ETIMEOUT; that call's
+ * output is incomplete), and clears it.
+ */
+int iqk_fp8_status(void* stream);
+
 #ifdef __cplusplus
 }
 #endif
