@@ -462,30 +462,29 @@ def _dense(t, shape, dtype, device, what: str):
     """t, or a new tensor where it is None: a contiguous CUDA tensor of this shape, type and device."""
     if t is None:
         return _empty(shape, dtype, device)
-    if t.dtype is not dtype or tuple(t.shape) != shape or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous {dtype} {list(shape)} on {device}, got {t.dtype} "
-                         f"{list(t.shape)} on {t.device}")
-    return t
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return t
+    raise ValueError(f"{what} must be a contiguous {dtype} {list(shape)} on {device}, got {t.dtype} "
+                     f"{list(t.shape)} on {t.device}")
 
 
-def _rows(t, what: str) -> int:
-    """Row stride of a CUDA matrix whose rows are contiguous."""
-    _need(t.is_cuda, f"{what} must be a CUDA tensor")
-    _need(t.dim() == 2, f"{what} must have two dimensions")
+def _rows(t, what: str):
+    """Shape and row stride of a CUDA matrix whose rows are contiguous."""
+    _need(t.is_cuda and t.dim() == 2, f"{what} must be a CUDA tensor of two dimensions")
     T, n = t.shape
-    _need(T == 0 or n == 1 or t.stride(1) == 1, f"{what} must have contiguous rows")
-    return t.stride(0) if T > 1 else n
+    stride, one = t.stride()
+    _need(one == 1 or n == 1 or T == 0, f"{what} must have contiguous rows")
+    return T, n, stride if T > 1 else n
 
 
 def _launch(fn, what: str, device, stream, *args) -> None:
     """Call an entry point on the tensors' device."""
-    torch = _torch()
+    C = _torch()._C
     at = device.index
-    if torch.cuda.current_device() != at:
-        with torch.cuda.device(at):
+    if C._cuda_getDevice() != at:
+        with _torch().cuda.device(at):
             return _launch(fn, what, device, stream, *args)
-    st = torch._C._cuda_getCurrentRawStream(at) if stream is None else stream.cuda_stream
-    rc = fn(*args, st)
+    rc = fn(*args, C._cuda_getCurrentRawStream(at) if stream is None else stream.cuda_stream)
     if rc:
         _check(rc, what)
 
@@ -496,17 +495,18 @@ def iqk_moe_topk(logits, topk: int, score: str = "softmax", bias=None, groups: i
     (float32 or bfloat16, rows may be strided): (ids int32 [T, topk], p float32
     [T, topk]), what iqk_moe_decode and iqk_moe_prefill take."""
     torch = _torch()
-    stride = _rows(logits, "logits")
-    _need(logits.dtype is torch.float32 or logits.dtype is torch.bfloat16, "logits must be float32 or bfloat16")
+    T, E, stride = _rows(logits, "logits")
+    dev, dt = logits.device, logits.dtype
+    _need(dt is torch.float32 or dt is torch.bfloat16, "logits must be float32 or bfloat16")
     _need(score in _SCORES, f"unknown score {score!r} (expected one of {sorted(_SCORES)})")
-    (T, E), dev = logits.shape, logits.device
     if bias is not None:
         _dense(bias, (E,), torch.float32, dev, "bias")
-    ids = _dense(ids, (T, topk), torch.int32, dev, "ids")
-    p = _dense(p, (T, topk), torch.float32, dev, "p")
-    _launch(lib().iqk_moe_topk, "iqk_moe_topk", dev, stream, logits.data_ptr(),
-            0 if logits.dtype is torch.float32 else 1, stride, T, E, topk, _SCORES[score], _ptr(bias), groups,
-            topk_groups, group_top, int(renorm), scale, ids.data_ptr(), p.data_ptr())
+    shape = (T, topk)
+    ids = _dense(ids, shape, torch.int32, dev, "ids")
+    p = _dense(p, shape, torch.float32, dev, "p")
+    _launch(lib().iqk_moe_topk, "iqk_moe_topk", dev, stream, logits.data_ptr(), 0 if dt is torch.float32 else 1, stride,
+            T, E, topk, _SCORES[score], None if bias is None else bias.data_ptr(), groups, topk_groups, group_top,
+            1 if renorm else 0, scale, ids.data_ptr(), p.data_ptr())
     return ids, p
 
 
@@ -514,9 +514,9 @@ def iqk_fp8_quantize(x, q=None, s=None, stream=None):
     """e4m3 codes and scales of bfloat16 x [T, cols] (rows may be strided), per
     row and 128 columns: (q float8_e4m3fn [T, cols], s float32 [T, ceil(cols / 128)])."""
     torch = _torch()
-    stride = _rows(x, "x")
+    T, cols, stride = _rows(x, "x")
+    dev = x.device
     _need(x.dtype is torch.bfloat16, "x must be bfloat16")
-    (T, cols), dev = x.shape, x.device
     q = _dense(q, (T, cols), torch.float8_e4m3fn, dev, "q")
     s = _dense(s, (T, (cols + 127) // 128), torch.float32, dev, "s")
     _launch(lib().iqk_fp8_quantize, "iqk_fp8_quantize", dev, stream, x.data_ptr(), stride, T, cols, q.data_ptr(),
@@ -524,35 +524,36 @@ def iqk_fp8_quantize(x, q=None, s=None, stream=None):
     return q, s
 
 
-def _fp8_operand(q, s, block_rows: int, what: str):
+def _fp8_operand(q, s, block_rows: int, device, what: str):
     """(rows, cols) of e4m3 codes q with their scales s per block_rows x 128 block."""
-    _need(q.is_cuda, f"{what} must be a CUDA tensor")
-    _need(q.dim() == 2, f"{what} must have two dimensions")
-    rows, cols = q.shape
-    _dense(q, (rows, cols), _torch().float8_e4m3fn, q.device, what)
-    _dense(s, ((rows + block_rows - 1) // block_rows, (cols + 127) // 128), _torch().float32, q.device,
-           f"{what}'s scales")
-    return rows, cols
+    _need(q.is_cuda and q.dim() == 2, f"{what} must be a CUDA tensor of two dimensions")
+    shape = rows, cols = q.shape
+    torch = _torch()
+    _dense(q, shape, torch.float8_e4m3fn, device, what)
+    _dense(s, ((rows + block_rows - 1) // block_rows, (cols + 127) // 128), torch.float32, device, "its scales")
+    return shape
 
 
 def iqk_fp8_linear(wq, ws, xq, xs, add=None, y=None, dtype=None, stream=None):
     """y = x w^T (+ add) [T, rows] of e4m3 operands: wq [rows, cols] with scales
     ws per 128 x 128 block, xq [T, cols] with scales xs as iqk_fp8_quantize
-    gives them. y is bfloat16 or float32 (`dtype`, bfloat16 unless y or add is
-    given); add has y's type and may be y."""
+    gives them. y is bfloat16 or float32 (`dtype`; by default y's or add's type,
+    else bfloat16); add has y's type and may be y."""
     torch = _torch()
-    rows, cols = _fp8_operand(wq, ws, 128, "wq")
-    T, xcols = _fp8_operand(xq, xs, 1, "xq")
     dev = wq.device
-    _need(xcols == cols and xq.device == dev, "xq must be [T, cols] on wq's device")
+    rows, cols = _fp8_operand(wq, ws, 128, dev, "wq")
+    T, xcols = _fp8_operand(xq, xs, 1, dev, "xq")
+    _need(xcols == cols, "xq must be [T, cols]")
     if dtype is None:
         dtype = y.dtype if y is not None else add.dtype if add is not None else torch.bfloat16
     _need(dtype is torch.bfloat16 or dtype is torch.float32, "y must be bfloat16 or float32")
+    shape = (T, rows)
     if add is not None:
-        _dense(add, (T, rows), dtype, dev, "add")
-    y = _dense(y, (T, rows), dtype, dev, "y")
+        _dense(add, shape, dtype, dev, "add")
+    y = _dense(y, shape, dtype, dev, "y")
     _launch(lib().iqk_fp8_linear, "iqk_fp8_linear", dev, stream, wq.data_ptr(), ws.data_ptr(), rows, cols,
-            xq.data_ptr(), xs.data_ptr(), T, _ptr(add), y.data_ptr(), 1 if dtype is torch.bfloat16 else 0)
+            xq.data_ptr(), xs.data_ptr(), T, None if add is None else add.data_ptr(), y.data_ptr(),
+            1 if dtype is torch.bfloat16 else 0)
     return y
 
 
@@ -561,11 +562,11 @@ def iqk_fp8_gate_up(gate_q, gate_s, up_q, up_s, xq, xs, q=None, s=None, stream=N
     [T, inter], s float32 [T, ceil(inter / 128)]), what iqk_fp8_linear takes as
     xq, xs for the down product."""
     torch = _torch()
-    inter, cols = _fp8_operand(gate_q, gate_s, 128, "gate_q")
-    _need(_fp8_operand(up_q, up_s, 128, "up_q") == (inter, cols), "gate_q and up_q must have one shape")
-    T, xcols = _fp8_operand(xq, xs, 1, "xq")
     dev = gate_q.device
-    _need(xcols == cols and xq.device == dev and up_q.device == dev, "xq must be [T, cols] on the weights' device")
+    shape = inter, cols = _fp8_operand(gate_q, gate_s, 128, dev, "gate_q")
+    _need(_fp8_operand(up_q, up_s, 128, dev, "up_q") == shape, "gate_q and up_q must have one shape")
+    T, xcols = _fp8_operand(xq, xs, 1, dev, "xq")
+    _need(xcols == cols, "xq must be [T, cols]")
     q = _dense(q, (T, inter), torch.float8_e4m3fn, dev, "q")
     s = _dense(s, (T, (inter + 127) // 128), torch.float32, dev, "s")
     _launch(lib().iqk_fp8_gate_up, "iqk_fp8_gate_up", dev, stream, gate_q.data_ptr(), gate_s.data_ptr(),

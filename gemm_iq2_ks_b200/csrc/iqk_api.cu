@@ -574,6 +574,7 @@ extern "C" int iqk_fp8_linear(const uint8_t* wq, const float* ws, int32_t rows, 
   a.cols = cols;
   a.nkb = fp8_blocks(cols);
   a.f32 = y_dtype == IQK_F32;
+  a.vec = rows % 4 == 0 && aligned(y, 4 * item) && aligned(add, 4 * item);
   return from_launch(launch_fp8_product(a, false, (cudaStream_t)stream, sms));
 }
 

@@ -9,6 +9,7 @@
 // are applied to each 128-column block's sum in float32 on the way into the
 // register accumulators.
 #include <algorithm>
+#include <atomic>
 
 #include "iqk_device.cuh"
 #include "iqk_internal.h"
@@ -56,6 +57,7 @@ __global__ void __launch_bounds__(kQuantThreads) k_fp8_quantize(const uint16_t* 
                                                                 int nkb, FastDiv by_nkb, int items,
                                                                 uint8_t* q, float* s) {
   griddep_wait();
+  griddep_launch();
   const int sub = threadIdx.x & 15;
   const int per = gridDim.x * (kQuantThreads / 16);
   for (int it0 = blockIdx.x * (kQuantThreads / 16) + (threadIdx.x >> 4); it0 < items; it0 += per * kQuantUnroll) {
@@ -157,108 +159,147 @@ __device__ __forceinline__ float magnitude(float h) {  // infinity for what is n
 }
 
 constexpr int kGemvMaxT = 16;
+constexpr size_t kGemvSmemMax = 110 * 1024;  // two CTAs in an SM's shared memory; beyond it the tiles take the call
 constexpr int kGemvRows = 16;
-constexpr int kGemvWarps(bool gu) { return gu ? 16 : 8; }  // at most
+constexpr int kGemvWarps = 8;  // at most; two CTAs fit an SM, so the next call's can start under this one's
 constexpr int kGuCluster = kFp8Block / kGemvRows;  // CTAs whose rows make up one scale's 128 columns of h
 
+// Shared memory: x rows (pitch nkb * 128 + 64 bytes, so that two neighbouring
+// tokens' pieces fall into different banks), the scales of x and of the
+// weights' blocks, then the warps' sums.
+__host__ __device__ inline int gemv_pitch(int nkb) { return nkb * kFp8Block + 64; }
+__host__ __device__ inline size_t gemv_x_bytes(int T, int nkb, int mats) {
+  return ((size_t)T * gemv_pitch(nkb) + (size_t)(T + mats) * nkb * 4 + 15) / 16 * 16;
+}
+
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+
 template <int NT, bool GU, int U>
-__global__ void __launch_bounds__(kGemvWarps(GU) * 32) k_fp8_gemv(const __grid_constant__ Fp8Args A) {
-  constexpr int M = GU ? 2 : 1;
-  extern __shared__ __align__(16) float gemv_smem[];  // [warps][M][8 NT tokens][16 rows]
+__global__ void __launch_bounds__(kGemvWarps * 32, NT == 1 ? 2 : 1) k_fp8_gemv(const __grid_constant__ Fp8Args A) {
+  constexpr int M = GU ? 2 : 1, TOK = 8 * NT;
+  extern __shared__ __align__(16) uint8_t gemv_smem[];
   __shared__ float s_amax[kGuCluster][kGemvMaxT];
   griddep_wait();
+  griddep_launch();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
   const int g = lane >> 2, tq = lane & 3;
   const int row0 = blockIdx.x * kGemvRows;
   if (GU) cluster_arrive();  // every CTA of the cluster runs before its shared memory is written to
-  float acc[M][NT][4] = {};
-  for (int kb0 = warp; kb0 < A.nkb; kb0 += nw * U) {
-    uint4 w[U][M][2][2], x[U][NT][2];  // weights: [row g, g + 8][64-column chunk]; x: [token g][chunk]
-    float sw[U][M], sx[U][NT][2];
+  const int pitch = gemv_pitch(A.nkb);
+  uint8_t* s_x = gemv_smem;
+  float* s_xs = reinterpret_cast<float*>(gemv_smem + (size_t)A.T * pitch);  // [T][nkb]
+  float* s_ws = s_xs + A.T * A.nkb;                                         // [M][nkb]
+  float* s_sum = reinterpret_cast<float*>(gemv_smem + gemv_x_bytes(A.T, A.nkb, M));
+
+  // Rows past the end read the last one's data; what they give is not stored.
+  const int rb = min(row0, A.rows - 1);
+  const uint8_t* wp[M][2];
 #pragma unroll
-    for (int u = 0; u < U; u++) {
-      const int kb = kb0 + u * nw;
-      const bool in = kb < A.nkb;
+  for (int m = 0; m < M; m++)
 #pragma unroll
-      for (int m = 0; m < M; m++) {
-        const Fp8Mat& W = m ? A.w1 : A.w0;
+    for (int r = 0; r < 2; r++)
+      wp[m][r] = (m ? A.w1.q : A.w0.q) + (int64_t)min(row0 + g + 8 * r, A.rows - 1) * A.cols + 16 * tq;
+  const int kleft = A.cols - 16 * tq;  // columns from this lane's first piece on
+  uint4 w[U][M][2][2];                 // U blocks in flight: [row g, g + 8][64-column chunk]
+  auto load = [&](int u, int kb) {
 #pragma unroll
-        for (int r = 0; r < 2; r++)
-#pragma unroll
-          for (int c = 0; c < 2; c++) {
-            const int row = row0 + g + 8 * r, k = kb * kFp8Block + 64 * c + 16 * tq;
-            w[u][m][r][c] = make_uint4(0, 0, 0, 0);
-            if (in && row < A.rows && k < A.cols)
-              w[u][m][r][c] = ld_u4(W.q + (int64_t)row * A.cols + k);
-          }
-        sw[u][m] = in && row0 < A.rows ? W.s[(int64_t)(row0 / kFp8Block) * A.nkb + kb] : 0.f;
-      }
-#pragma unroll
-      for (int n = 0; n < NT; n++) {
-#pragma unroll
-        for (int c = 0; c < 2; c++) {
-          const int tok = 8 * n + g, k = kb * kFp8Block + 64 * c + 16 * tq;
-          x[u][n][c] = make_uint4(0, 0, 0, 0);
-          if (in && tok < A.T && k < A.cols)
-            x[u][n][c] = ld_u4(A.xq + (int64_t)tok * A.cols + k);
-        }
-#pragma unroll
-        for (int j = 0; j < 2; j++) {
-          const int tok = 8 * n + 2 * tq + j;
-          sx[u][n][j] = in && tok < A.T ? A.xs[(int64_t)tok * A.nkb + kb] : 0.f;
-        }
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < U; u++) {
-      if (kb0 + u * nw >= A.nkb) break;
+    for (int c = 0; c < 2; c++) {
+      const int k = kb * kFp8Block + 64 * c;
+      const bool in = k < kleft;  // false as well for kb past the last block
 #pragma unroll
       for (int m = 0; m < M; m++)
 #pragma unroll
-        for (int n = 0; n < NT; n++) {
-          float d[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int r = 0; r < 2; r++) {
+          w[u][m][r][c] = make_uint4(0, 0, 0, 0);
+          if (in) w[u][m][r][c] = *reinterpret_cast<const uint4*>(wp[m][r] + k);
+        }
+    }
+  };
 #pragma unroll
-          for (int c = 0; c < 2; c++) {
-            const uint4 a = w[u][m][0][c], b = w[u][m][1][c], v = x[u][n][c];
-            mma_e4m3(d, a.x, b.x, a.y, b.y, v.x, v.y);
-            mma_e4m3(d, a.z, b.z, a.w, b.w, v.z, v.w);
-          }
+  for (int u = 0; u < U; u++) load(u, warp + u * nw);
+
+  // x and the scales, while the first weights are on their way
+  for (int t = 0; t < A.T; t++)
+    for (int k = threadIdx.x * 16; k < A.nkb * kFp8Block; k += blockDim.x * 16) {
+      if (k < A.cols)
+        cp_async16(s_x + t * pitch + k, A.xq + (int64_t)t * A.cols + k);
+      else
+        *reinterpret_cast<uint4*>(s_x + t * pitch + k) = make_uint4(0, 0, 0, 0);
+    }
+  for (int i = threadIdx.x; i < A.T * A.nkb; i += blockDim.x) s_xs[i] = A.xs[i];
+  for (int i = threadIdx.x; i < A.nkb; i += blockDim.x) {
+#pragma unroll
+    for (int m = 0; m < M; m++) s_ws[m * A.nkb + i] = (m ? A.w1.s : A.w0.s)[(int64_t)(rb / kFp8Block) * A.nkb + i];
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncthreads();
+
+  float acc[M][NT][4] = {};
+  const uint8_t* xr[NT];
+  int st[NT][2];
+#pragma unroll
+  for (int n = 0; n < NT; n++) {
+    xr[n] = s_x + min(8 * n + g, A.T - 1) * pitch + 16 * tq;
+#pragma unroll
+    for (int j = 0; j < 2; j++) st[n][j] = min(8 * n + 2 * tq + j, A.T - 1) * A.nkb;
+  }
+  for (int kb0 = warp; kb0 < A.nkb; kb0 += nw * U) {
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+      const int kb = kb0 + u * nw;
+      if (kb >= A.nkb) break;
+#pragma unroll
+      for (int n = 0; n < NT; n++) {
+        const uint4 x0 = *reinterpret_cast<const uint4*>(xr[n] + kb * kFp8Block);
+        const uint4 x1 = *reinterpret_cast<const uint4*>(xr[n] + kb * kFp8Block + 64);
+        const float sx0 = s_xs[st[n][0] + kb], sx1 = s_xs[st[n][1] + kb];
+#pragma unroll
+        for (int m = 0; m < M; m++) {
+          float d[4] = {0.f, 0.f, 0.f, 0.f};
+          const uint4 a0 = w[u][m][0][0], b0 = w[u][m][1][0], a1 = w[u][m][0][1], b1 = w[u][m][1][1];
+          mma_e4m3(d, a0.x, b0.x, a0.y, b0.y, x0.x, x0.y);
+          mma_e4m3(d, a0.z, b0.z, a0.w, b0.w, x0.z, x0.w);
+          mma_e4m3(d, a1.x, b1.x, a1.y, b1.y, x1.x, x1.y);
+          mma_e4m3(d, a1.z, b1.z, a1.w, b1.w, x1.z, x1.w);
           // d: (row g, tokens 2 tq, 2 tq + 1), (row g + 8, the same)
-          const float s0 = sw[u][m] * sx[u][n][0], s1 = sw[u][m] * sx[u][n][1];
+          const float sw = s_ws[m * A.nkb + kb], s0 = sw * sx0, s1 = sw * sx1;
           acc[m][n][0] += d[0] * s0;
           acc[m][n][1] += d[1] * s1;
           acc[m][n][2] += d[2] * s0;
           acc[m][n][3] += d[3] * s1;
         }
+      }
+      load(u, kb + U * nw);
     }
   }
-  constexpr int TOK = 8 * NT;
 #pragma unroll
   for (int m = 0; m < M; m++)
 #pragma unroll
     for (int n = 0; n < NT; n++)
 #pragma unroll
       for (int j = 0; j < 4; j++)
-        gemv_smem[((warp * M + m) * TOK + 8 * n + 2 * tq + (j & 1)) * kGemvRows + g + 8 * (j >> 1)] = acc[m][n][j];
+        s_sum[((warp * M + m) * TOK + 8 * n + 2 * tq + (j & 1)) * kGemvRows + g + 8 * (j >> 1)] = acc[m][n][j];
   __syncthreads();
   // Warps' sums in order; 16 consecutive lanes hold one token's 16 rows.
   if (!GU) {
     for (int i = threadIdx.x; i < A.T * kGemvRows; i += blockDim.x) {
       float v = 0.f;
-      for (int k = 0; k < nw; k++) v += gemv_smem[k * TOK * kGemvRows + i];
+      for (int k = 0; k < nw; k++) v += s_sum[k * TOK * kGemvRows + i];
       const int tok = i / kGemvRows, row = row0 + i % kGemvRows;
       if (row < A.rows) put_y(A, (int64_t)tok * A.rows + row, v);
     }
     return;
   }
-  float* hbuf = gemv_smem + (size_t)nw * M * TOK * kGemvRows;  // [tokens][16]
+  float* hbuf = s_sum + (size_t)nw * M * TOK * kGemvRows;  // [tokens][16]
   const uint32_t rank = cluster_rank();
   cluster_wait();
   for (int i = threadIdx.x; i < TOK * kGemvRows; i += blockDim.x) {  // whole half-warps
     float gv = 0.f, uv = 0.f;
     for (int k = 0; k < nw; k++) {
-      gv += gemv_smem[(k * M) * TOK * kGemvRows + i];
-      uv += gemv_smem[(k * M + M - 1) * TOK * kGemvRows + i];
+      gv += s_sum[(k * M) * TOK * kGemvRows + i];
+      uv += s_sum[(k * M + M - 1) * TOK * kGemvRows + i];
     }
     const float h = silu_f32(gv) * uv;
     hbuf[i] = h;
@@ -292,26 +333,39 @@ __global__ void __launch_bounds__(kGemvWarps(GU) * 32) k_fp8_gemv(const __grid_c
 // tcgen05 tiles of 128 tokens x BN weight rows (gate_up: 128 gate and 128 up
 // rows side by side). One 128-column block is one pipeline step: TMA brings
 // both operands' 128-byte rows (128-byte swizzle), four MMAs leave the block's
-// sums in one of the tensor-memory buffers, and two warpgroups add them, times
-// the two scales, to float32 accumulators in registers (thread = token row;
-// each warpgroup half of the columns). With few tiles the CTAs of a cluster
-// split the blocks and add their accumulators over distributed shared memory,
-// in rank order.
+// sums in one of the tensor-memory buffers, and 16 warps add them, times the two scales, to float32 accumulators
+// in registers (thread = token row; a quarter of the columns for each four
+// warps). CTAs are persistent over tiles:
+// the copies and MMAs of the next tile run while this one is stored. With few
+// tiles the CTAs of a cluster split the blocks of one tile and add their
+// accumulators over distributed shared memory, in rank order.
 constexpr int kBM = 128;
-constexpr int kEpiWarps = 8, kTmaWarp = 8, kMmaWarp = 9;
-constexpr int kGemmThreads = 10 * 32;
+constexpr int kEpiWarps = 16, kTmaWarp = 16, kMmaWarp = 17;
+constexpr int kGemmThreads = 20 * 32;  // the last warpgroup: copies, MMAs and two idle warps
+// Registers: 640 threads are launched with 96 each; the accumulating warps take
+// 112, the last warpgroup keeps 32 (4 x 112 + 32 = 5 x 96).
+constexpr int kEpiRegs = 112, kLastRegs = 32;
 constexpr int kGemmStageBytes(int BN) { return (kBM + BN) * kFp8Block; }
 constexpr int kGemmStages(int BN) { return BN == 256 ? 4 : 6; }
+constexpr int kGemmRing(int BN) { return kGemmStages(BN) * kGemmStageBytes(BN); }
 constexpr int kPitch(int BN) { return BN + 4; }  // floats between rows of the shared accumulators
-constexpr size_t kGemmSmem(int BN) {
-  const size_t a = (size_t)kGemmStages(BN) * kGemmStageBytes(BN), b = (size_t)kBM * kPitch(BN) * 4;
-  return (a > b ? a : b) + 256 + 1024;
-}
+constexpr int kStageOut = 2048;                  // bytes of one warp's store staging: 32 rows x 16 floats
+constexpr size_t kGemmSmem(int BN) { return kGemmRing(BN) + kEpiWarps * kStageOut + 256 + 1024; }
+static_assert(kBM * kPitch(256) * 4 <= kGemmRing(256) && kBM * kPitch(128) * 4 <= kGemmRing(128), "accumulators");
 
+// Bounded wait: gives up after kDefaultWaitNs of the global timer, or soon
+// after another warp of the CTA did.
 __device__ __forceinline__ bool gemm_wait(uint64_t* bar, uint32_t par, volatile uint32_t* abort_flag) {
-  for (uint32_t i = 0; i < (1u << 24); i++) {
+  if (mbar_try_wait(bar, par)) return true;
+  uint64_t t0 = 0;
+  for (uint32_t i = 1;; i++) {
     if (mbar_try_wait(bar, par)) return true;
-    if ((i & 1023u) == 1023u && *abort_flag) return false;
+    if (i % 256 == 0) {
+      if (*abort_flag) return false;
+      const uint64_t now = globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 >= kDefaultWaitNs) break;
+    }
   }
   *abort_flag = 1;
   atomicOr(&g_fp8_status, 2);
@@ -328,6 +382,14 @@ __device__ __forceinline__ void mma_ss_e4m3(uint32_t d_tmem, uint64_t a_desc, ui
       : "memory");
 }
 
+// One lane of a converged warp: the copies and MMAs are issued under it, from
+// code that the whole warp runs.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
@@ -341,15 +403,28 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
 // The wait names the loaded registers, so that nothing reads them ahead of it.
 __device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
-                   "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
-                   "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
-                   "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
-                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
-                   "+r"(r[30]), "+r"(r[31])
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
+                 "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31])
                :
                : "memory");
 }
+
+// Two float32 fused multiply-adds in one instruction: acc += (lo, hi) * (s, s).
+__device__ __forceinline__ void fma2(uint64_t& acc, uint32_t lo, uint32_t hi, uint64_t s) {
+  asm("{\n\t.reg .b64 v;\n\tmov.b64 v, {%1, %2};\n\tfma.rn.f32x2 %0, v, %3, %0;\n\t}"
+      : "+l"(acc)
+      : "r"(lo), "r"(hi), "l"(s));
+}
+__device__ __forceinline__ uint64_t twice(float s) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(s));
+  return r;
+}
+__device__ __forceinline__ float lo_of(uint64_t v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float hi_of(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
 
 // Instruction descriptor, kind::f8f6f4: e4m3 A and B (format code 0), float32
 // accumulator, both K-major, M = 128, N = n.
@@ -357,25 +432,56 @@ __host__ __device__ constexpr uint32_t idesc_e4m3_m128(uint32_t n) {
   return (1u << 4) | ((n >> 3) << 17) | ((128u >> 4) << 24);
 }
 
+// Four neighbouring outputs of one row; A.vec: rows and pointers allow vector access.
+__device__ __forceinline__ void put_y4(const Fp8Args& A, int64_t t, int n, float4 v) {
+  const int64_t i = t * A.rows + n;
+  if (!A.vec) {
+    const float w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int c = 0; c < 4; c++)
+      if (n + c < A.rows) put_y(A, i + c, w[c]);
+    return;
+  }
+  if (n >= A.rows) return;
+  if (A.f32) {
+    if (A.add) {
+      const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(A.add) + i);
+      v = make_float4(v.x + a.x, v.y + a.y, v.z + a.z, v.w + a.w);
+    }
+    *reinterpret_cast<float4*>(static_cast<float*>(A.y) + i) = v;
+  } else {
+    if (A.add) {
+      const uint2 a = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(A.add) + i);
+      v.x += __uint_as_float(a.x << 16);
+      v.y += __uint_as_float(a.x & 0xffff0000u);
+      v.z += __uint_as_float(a.y << 16);
+      v.w += __uint_as_float(a.y & 0xffff0000u);
+    }
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(A.y) + i) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+  }
+}
+
 template <int BN, bool GU>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     k_fp8_gemm(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap m0,
-               const __grid_constant__ CUtensorMap m1, const __grid_constant__ Fp8Args A, int tiles_m, int split) {
-  constexpr int ST = kGemmStages(BN), SB = kGemmStageBytes(BN), NBUF = 512 / BN, NC = BN / 2;
+               const __grid_constant__ CUtensorMap m1, const __grid_constant__ Fp8Args A, int tiles_m, int tiles,
+               int split) {
+  constexpr int ST = kGemmStages(BN), SB = kGemmStageBytes(BN), NC = BN / 4;
+  constexpr int NBUF = 512 / BN;  // accumulators in tensor memory
   constexpr int NB = GU ? 128 : BN;  // output columns of a tile
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kGemmSmem(BN) - 256 - 1024);
+  uint8_t* staging = smem + kGemmRing(BN);
+  uint64_t* full = reinterpret_cast<uint64_t*>(staging + kEpiWarps * kStageOut);
   uint64_t* empty = full + ST;
   uint64_t* tfull = empty + ST;
-  uint64_t* tfree = tfull + NBUF;
-  uint64_t* drain = tfree + NBUF;
+  uint64_t* tfree = tfull + 4;
+  uint64_t* drain = tfree + 4;
   uint32_t* holder = reinterpret_cast<uint32_t*>(drain + 1);
   volatile uint32_t* abort_flag = holder + 1;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const int rank = split > 1 ? (int)cluster_rank() : 0;
-  const int tile = blockIdx.x / split;
-  const int t0 = (tile % tiles_m) * kBM, n0 = (tile / tiles_m) * NB;
+  const int first = blockIdx.x / split, step = gridDim.x / split;
   const int kb_lo = (int)((int64_t)A.nkb * rank / split), kb_hi = (int)((int64_t)A.nkb * (rank + 1) / split);
   const int steps = kb_hi - kb_lo;
 
@@ -403,119 +509,225 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *holder;
   griddep_wait();
+  griddep_launch();
 
-  if (warp == kTmaWarp) {
-    if (lane == 0) {
-      int i = 0;
-      for (; i < steps; i++) {
-        const int s = i % ST, k = (kb_lo + i) * kFp8Block;
-        if (!gemm_wait(&empty[s], ((i / ST) & 1) ^ 1, abort_flag)) break;
-        uint8_t* a = smem + s * SB;
-        mbar_arrive_expect_tx(&full[s], SB);
-        tma_load_2d(a, &mx, k, t0, &full[s]);
-        tma_load_2d(a + kBM * kFp8Block, &m0, k, n0, &full[s]);
-        if (BN == 256) tma_load_2d(a + (kBM + 128) * kFp8Block, &m1, k, GU ? n0 : n0 + 128, &full[s]);
-      }
-      if (i < steps)  // a wait expired: let the copies in flight land
-        for (int j = i < ST ? 0 : i - ST; j < i; j++) mbar_wait_bounded(&full[j % ST], (j / ST) & 1);
-    }
-  } else if (warp == kMmaWarp) {
-    if (lane == 0) {
-      int i = 0;
-      for (; i < steps; i++) {
-        const int s = i % ST, b = i % NBUF;
-        if (!gemm_wait(&full[s], (i / ST) & 1, abort_flag)) break;
-        if (!gemm_wait(&tfree[b], ((i / NBUF) & 1) ^ 1, abort_flag)) break;
-        tc_fence_after();
-        const uint32_t a = smem_u32(smem + s * SB);
-#pragma unroll
-        for (int j = 0; j < 4; j++)
-          mma_ss_e4m3(tmem + b * BN, sdesc_kmajor_sw128(a + 32u * j),
-                      sdesc_kmajor_sw128(a + kBM * kFp8Block + 32u * j), idesc_e4m3_m128(BN), j != 0);
-        tc_commit(&empty[s]);
-        tc_commit(&tfull[b]);
-      }
-      if (i < steps) {  // a wait expired: let the products in flight end before their tensor memory is given back
-        tc_commit(drain);
-        mbar_wait_bounded(drain, 0);
-      }
-    }
-  } else {
-    const int half = warp >> 2, q = warp & 3;
-    const int t = t0 + 32 * q + lane;
-    const bool rows_in = t0 + 32 * q < A.T;  // some row of this warp exists
-    const Fp8Mat& W = GU && half ? A.w1 : A.w0;
-    // the weight block of this warpgroup's columns (past the last: any, its columns are not stored)
-    const int wb = min((n0 + (GU || BN == 128 ? 0 : 128 * half)) / kFp8Block, (A.rows - 1) / kFp8Block);
-    const float* ws = W.s + (int64_t)wb * A.nkb + kb_lo;
-    const float* xs = A.xs + (int64_t)min(t, A.T - 1) * A.nkb + kb_lo;
-    float acc[NC];
-#pragma unroll
-    for (int c = 0; c < NC; c++) acc[c] = 0.f;
-    bool ok = true;
-    float sc = steps > 0 ? ws[0] * xs[0] : 0.f;
-    for (int i = 0; i < steps && ok; i++) {
-      const int b = i % NBUF;
-      const float sn = i + 1 < steps ? ws[i + 1] * xs[i + 1] : 0.f;
-      ok = gemm_wait(&tfull[b], (i / NBUF) & 1, abort_flag);
-      tc_fence_after();
-      if (rows_in) {
-        const uint32_t base = tmem + ((uint32_t)(32 * q) << 16) + b * BN + half * NC;
-#pragma unroll
-        for (int c0 = 0; c0 < NC; c0 += 32) {
-          uint32_t r[32];
-          tmem_ld32(base + c0, r);
-          tmem_wait_ld(r);
-#pragma unroll
-          for (int c = 0; c < 32; c++) acc[c0 + c] += __uint_as_float(r[c]) * sc;
+  if (warp >= kEpiWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLastRegs));
+    if (warp == kTmaWarp) {
+      const bool leader = elect_one();
+      int it = 0;
+      bool ok = true;
+      for (int tile = first; tile < tiles && ok; tile += step) {
+        const int t0 = (tile % tiles_m) * kBM, n0 = (tile / tiles_m) * NB;
+        for (int i = 0; i < steps; i++, it++) {
+          const int s = it % ST, k = (kb_lo + i) * kFp8Block;
+          if (!(ok = gemm_wait(&empty[s], ((it / ST) & 1) ^ 1, abort_flag))) break;
+          if (leader) {
+            uint8_t* a = smem + s * SB;
+            uint8_t* w = a + kBM * kFp8Block;
+            mbar_arrive_expect_tx(&full[s], SB);
+            tma_load_2d(a, &mx, k, t0, &full[s]);
+            tma_load_2d(w, &m0, k, n0, &full[s]);
+            if (BN == 256) tma_load_2d(w + 128 * kFp8Block, &m1, k, GU ? n0 : n0 + 128, &full[s]);
+          }
+          __syncwarp();
         }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&tfree[b]);
-      sc = sn;
+      if (!ok)  // a wait expired: let the copies in flight land
+        for (int j = it < ST ? 0 : it - ST; j < it; j++) mbar_wait_ns(&full[j % ST], (j / ST) & 1, kDrainWaitNs);
     }
-    // All MMAs have read their operands: the stages take the accumulators.
-    if (rows_in && ok) {
-      float* dst = reinterpret_cast<float*>(smem) + (size_t)(32 * q + lane) * kPitch(BN) + half * NC;
+    if (warp == kMmaWarp) {
+      const bool leader = elect_one();
+      // descriptors differ in the address field (bytes / 16) only
+      const uint64_t d0 = sdesc_kmajor_sw128(smem_u32(smem));
+      int it = 0;
+      bool ok = true;
+      for (int tile = first; tile < tiles && ok; tile += step) {
+        for (int i = 0; i < steps; i++, it++) {
+          const int s = it % ST, b = it % NBUF;
+          if (!(ok = gemm_wait(&full[s], (it / ST) & 1, abort_flag) &&
+                     gemm_wait(&tfree[b], ((it / NBUF) & 1) ^ 1, abort_flag)))
+            break;
+          tc_fence_after();
+          if (leader) {
+            const uint64_t da = d0 + (uint32_t)(s * (SB / 16)), dw = da + kBM * kFp8Block / 16;
 #pragma unroll
-      for (int c = 0; c < NC; c += 4)
-        *reinterpret_cast<float4*>(dst + c) = make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]);
+            for (int j = 0; j < 4; j++) mma_ss_e4m3(tmem + b * BN, da + 2u * j, dw + 2u * j, idesc_e4m3_m128(BN), j != 0);
+            tc_commit(&tfull[b]);
+            tc_commit(&empty[s]);
+          }
+          __syncwarp();
+        }
+      }
+      if (!ok) {  // a wait expired: let the products in flight end before their tensor memory is given back
+        if (leader) tc_commit(drain);
+        mbar_wait_ns(drain, 0, kDrainWaitNs);
+      }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+    if (split > 1) {  // the two cluster barriers of the other warps
+      cluster_arrive();
+      cluster_wait();
+      cluster_arrive();
+      cluster_wait();
+    }
+    return;
+  }
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
+  {
+    // Lanes 32 q .. 32 q + 31 of tensor memory; columns part * NC and on of the
+    // block, for gate_up 32 gate columns and the same 32 up columns.
+    const int q = warp & 3, part = warp >> 2;
+    const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16);
+    int it = 0;
+    bool ok = true;
+    for (int tile = first; tile < tiles && ok; tile += step) {
+      const int t0 = (tile % tiles_m) * kBM, n0 = (tile / tiles_m) * NB;
+      const int t = t0 + 32 * q + lane;
+      const bool rows_in = t0 + 32 * q < A.T;  // some row of this warp exists
+      // the weight block of this warp's columns (past the last: any, its columns are not stored)
+      const int wb = min((n0 + (BN == 256 && !GU ? part * NC : 0)) / kFp8Block, (A.rows - 1) / kFp8Block);
+      const float* ws = A.w0.s + (int64_t)wb * A.nkb + kb_lo;
+      const float* us = A.w1.s + (int64_t)wb * A.nkb + kb_lo;
+      const float* xs = A.xs + (int64_t)min(t, A.T - 1) * A.nkb + kb_lo;
+      uint64_t acc[NC / 2];
+#pragma unroll
+      for (int c = 0; c < NC / 2; c++) acc[c] = 0;
+      float xn = xs[0], wn = ws[0], un = GU ? us[0] : 0.f;
+      for (int i = 0; i < steps; i++, it++) {
+        const int b = it % NBUF;
+        const uint64_t sw = twice(xn * wn), su = GU ? twice(xn * un) : sw;
+        if (i + 1 < steps) {
+          xn = xs[i + 1];
+          wn = ws[i + 1];
+          if (GU) un = us[i + 1];
+        }
+        if (!(ok = gemm_wait(&tfull[b], (it / NBUF) & 1, abort_flag))) break;
+        tc_fence_after();
+        if (rows_in) {
+          const uint32_t col = lanes + b * BN + (GU ? part * 32 : part * NC);
+#pragma unroll
+          for (int c0 = 0; c0 < NC; c0 += 32) {
+            uint32_t r[32];
+            tmem_ld32(col + (GU && c0 ? 128 : c0), r);
+            tmem_wait_ld(r);
+#pragma unroll
+            for (int c = 0; c < 16; c++) fma2(acc[c0 / 2 + c], r[2 * c], r[2 * c + 1], c0 ? su : sw);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&tfree[b]);
+      }
+      if (!ok) break;
+      if (split > 1) {
+        // All MMAs have read their operands: the ring takes the accumulators.
+        if (rows_in) {
+          float* dst = reinterpret_cast<float*>(smem) + (size_t)(32 * q + lane) * kPitch(BN);
+#pragma unroll
+          for (int c = 0; c < NC; c += 4)
+            *reinterpret_cast<float4*>(dst + (GU ? part * 32 + (c < 32 ? c : 96 + c) : part * NC + c)) =
+                make_float4(lo_of(acc[c / 2]), hi_of(acc[c / 2]), lo_of(acc[c / 2 + 1]), hi_of(acc[c / 2 + 1]));
+        }
+      } else if (GU) {
+        // h in the thread; the row's largest magnitude over the four warps with its columns
+        float h[32], most = 0.f;
+        const int n = n0 + part * 32;
+#pragma unroll
+        for (int c = 0; c < 32; c++) {
+          const float g = (c & 1) ? hi_of(acc[c / 2]) : lo_of(acc[c / 2]);
+          const float u = (c & 1) ? hi_of(acc[NC / 4 + c / 2]) : lo_of(acc[NC / 4 + c / 2]);
+          h[c] = silu_f32(g) * u;
+        }
+#pragma unroll
+        for (int c = 0; c < 32; c += 16)  // rows is a multiple of 16
+          if (n + c < A.rows) {
+#pragma unroll
+            for (int j = 0; j < 16; j++) most = fmaxf(most, magnitude(h[c + j]));
+          }
+        float* smost = reinterpret_cast<float*>(staging);  // [4 parts][128 rows]
+        smost[part * kBM + 32 * q + lane] = most;
+        asm volatile("bar.sync %0, 128;" ::"r"(1 + q) : "memory");
+#pragma unroll
+        for (int k = 0; k < 4; k++) most = fmaxf(most, smost[k * kBM + 32 * q + lane]);
+        asm volatile("bar.sync %0, 128;" ::"r"(1 + q) : "memory");
+        const bool fine = most <= 3.402823466e38f;
+        most = fmaxf(most, kAmaxMin);
+        const float inv = fine ? kE4m3Max / most : 0.f;
+        if (t < A.T) {
+#pragma unroll
+          for (int c = 0; c < 32; c += 16)
+            if (n + c < A.rows) {
+              uint32_t o[4];
+#pragma unroll
+              for (int j = 0; j < 4; j++)
+                o[j] = fine ? e4m3x4(h[c + 4 * j] * inv, h[c + 4 * j + 1] * inv, h[c + 4 * j + 2] * inv,
+                                     h[c + 4 * j + 3] * inv)
+                            : 0u;
+              *reinterpret_cast<uint4*>(static_cast<uint8_t*>(A.y) + (int64_t)t * A.rows + n + c) =
+                  make_uint4(o[0], o[1], o[2], o[3]);
+            }
+          if (part == 0)
+            A.hs[(int64_t)t * ((A.rows + kFp8Block - 1) / kFp8Block) + n0 / kFp8Block] =
+                fine ? most / kE4m3Max : __int_as_float(0x7fffffff);
+        }
+      } else if (rows_in) {
+        // Through the warp's staging, 16 columns at a time, to stores of whole
+        // 32-byte sectors; 16-byte pieces are permuted against bank conflicts.
+        float* st = reinterpret_cast<float*>(staging + warp * kStageOut);
+#pragma unroll
+        for (int c0 = 0; c0 < NC; c0 += 16) {
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 4; j++) {
+            const int c = (c0 + 4 * j) / 2;
+            *reinterpret_cast<float4*>(st + lane * 16 + 4 * (j ^ ((lane >> 1) & 3))) =
+                make_float4(lo_of(acc[c]), hi_of(acc[c]), lo_of(acc[c + 1]), hi_of(acc[c + 1]));
+          }
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 4; i++) {
+            const int r = 8 * i + (lane >> 2), j = lane & 3;
+            const float4 v = *reinterpret_cast<const float4*>(st + r * 16 + 4 * (j ^ ((r >> 1) & 3)));
+            const int64_t tr = t0 + 32 * q + r;
+            if (tr < A.T) put_y4(A, tr, n0 + part * NC + c0 + 4 * j, v);
+          }
+        }
+      }
     }
   }
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
-  tc_fence_after();
-  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
-  if (split > 1) {
-    cluster_arrive();
-    cluster_wait();
-  }
+  if (split == 1) return;
+
+  cluster_arrive();
+  cluster_wait();
   // One warp per row, rows dealt to the cluster's CTAs and their warps in turn.
+  const int t0 = (first % tiles_m) * kBM, n0 = (first / tiles_m) * NB;
   const int nrow = min(kBM, A.T - t0);
-  const int hblocks = (A.rows + kFp8Block - 1) / kFp8Block;
-  for (int r = rank + split * warp; r < nrow; r += split * (kGemmThreads / 32)) {
+  for (int r = rank + split * warp; r < nrow; r += split * kEpiWarps) {
     float4 v[BN / 128];
 #pragma unroll
     for (int h = 0; h < BN / 128; h++) {
       const float* src = reinterpret_cast<const float*>(smem) + (size_t)r * kPitch(BN) + 128 * h + 4 * lane;
-      if (split == 1) {
-        v[h] = *reinterpret_cast<const float4*>(src);
-      } else {
-        v[h] = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int k = 0; k < split; k++) {
-          const float4 o = ld_peer4(peer_smem(src, k));
-          v[h].x += o.x;
-          v[h].y += o.y;
-          v[h].z += o.z;
-          v[h].w += o.w;
-        }
+      v[h] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int k = 0; k < split; k++) {
+        const float4 o = ld_peer4(peer_smem(src, k));
+        v[h].x += o.x;
+        v[h].y += o.y;
+        v[h].z += o.z;
+        v[h].w += o.w;
       }
     }
     const int64_t t = t0 + r;
+    const int n = n0 + 4 * lane;
     if (GU) {
       const float4 gv = v[0], uv = v[BN / 128 - 1];
-      const int n = n0 + 4 * lane;  // rows is a multiple of 16: all four columns exist or none
       const float h0 = silu_f32(gv.x) * uv.x, h1 = silu_f32(gv.y) * uv.y, h2 = silu_f32(gv.z) * uv.z,
                   h3 = silu_f32(gv.w) * uv.w;
       float most =
@@ -527,22 +739,16 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       const float inv = fine ? kE4m3Max / most : 0.f;
       const uint32_t o = fine ? e4m3x4(h0 * inv, h1 * inv, h2 * inv, h3 * inv) : 0u;
       if (n < A.rows) *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(A.y) + t * A.rows + n) = o;
-      if (lane == 0) A.hs[t * hblocks + n0 / kFp8Block] = fine ? most / kE4m3Max : __int_as_float(0x7fffffff);
+      if (lane == 0)
+        A.hs[t * ((A.rows + kFp8Block - 1) / kFp8Block) + n0 / kFp8Block] =
+            fine ? most / kE4m3Max : __int_as_float(0x7fffffff);
     } else {
 #pragma unroll
-      for (int h = 0; h < BN / 128; h++) {
-        const int n = n0 + 128 * h + 4 * lane;
-        const float w[4] = {v[h].x, v[h].y, v[h].z, v[h].w};
-#pragma unroll
-        for (int c = 0; c < 4; c++)
-          if (n + c < A.rows) put_y(A, t * A.rows + n + c, w[c]);
-      }
+      for (int h = 0; h < BN / 128; h++) put_y4(A, t, n + 128 * h, v[h]);
     }
   }
-  if (split > 1) {  // the peers have read this CTA's accumulators
-    cluster_arrive();
-    cluster_wait();
-  }
+  cluster_arrive();  // the peers have read this CTA's accumulators
+  cluster_wait();
 }
 
 cudaLaunchAttribute pdl() {
@@ -560,19 +766,37 @@ cudaLaunchAttribute cluster_of(int n) {
   return a;
 }
 
+// Lets the kernel use BYTES of dynamic shared memory, once per device (a second thread may repeat it).
+template <auto KERN, size_t BYTES>
+int allow_smem() {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return -4;
+  if (dev < 64 && (done.load(std::memory_order_relaxed) >> dev & 1)) return 0;
+  if (cudaFuncSetAttribute(KERN, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)BYTES) != cudaSuccess) return -4;
+  if (dev < 64) done.fetch_or(1ull << dev, std::memory_order_relaxed);
+  return 0;
+}
+
+size_t gemv_smem_bytes(int T, int nkb, int nw, int nt, bool gu) {
+  return gemv_x_bytes(T, nkb, gu ? 2 : 1) + (size_t)(nw * (gu ? 2 : 1) + (gu ? 1 : 0)) * 8 * nt * kGemvRows * 4;
+}
+
 template <int NT, bool GU, int U>
 int launch_gemv_nt(const Fp8Args& a, cudaStream_t st) {
-  const int nw = std::min(kGemvWarps(GU), (a.nkb + U - 1) / U);
+  const int nw = std::min(kGemvWarps, (a.nkb + U - 1) / U);
   const int tiles = (a.rows + kGemvRows - 1) / kGemvRows;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(GU ? (tiles + kGuCluster - 1) / kGuCluster * kGuCluster : tiles));
   cfg.blockDim = dim3((unsigned)nw * 32);
-  cfg.dynamicSmemBytes = (size_t)(nw * (GU ? 2 : 1) + (GU ? 1 : 0)) * 8 * NT * kGemvRows * 4;
+  cfg.dynamicSmemBytes = gemv_smem_bytes(a.T, a.nkb, nw, NT, GU);
+  auto kern = k_fp8_gemv<NT, GU, U>;
+  if (cfg.dynamicSmemBytes > 47 * 1024 && allow_smem<k_fp8_gemv<NT, GU, U>, kGemvSmemMax>()) return -4;
   cfg.stream = st;
   cudaLaunchAttribute at[2] = {pdl(), cluster_of(kGuCluster)};
   cfg.attrs = at;
   cfg.numAttrs = GU ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, k_fp8_gemv<NT, GU, U>, a) == cudaSuccess ? 0 : -4;
+  return cudaLaunchKernelEx(&cfg, kern, a) == cudaSuccess ? 0 : -4;
 }
 
 // Map of a row-major e4m3 matrix, boxes of 128 rows x 128 columns; columns and rows past the end read as zero.
@@ -597,21 +821,27 @@ int launch_gemm(const Fp8Args& a, int num_sms, cudaStream_t st) {
   int split = 1;
   while (split < 8 && tiles * split * 2 <= num_sms && split * 2 <= a.nkb) split *= 2;
   CUtensorMap mx, m0, m1;
-  if (make_e4m3_map(&mx, a.xq, a.T, a.cols) || make_e4m3_map(&m0, a.w0.q, a.rows, a.cols) ||
-      make_e4m3_map(&m1, GU ? a.w1.q : a.w0.q, a.rows, a.cols))
-    return -4;
+  if (make_e4m3_map(&mx, a.xq, a.T, a.cols) || make_e4m3_map(&m0, a.w0.q, a.rows, a.cols)) return -4;
+  if (GU ? make_e4m3_map(&m1, a.w1.q, a.rows, a.cols) != 0 : (m1 = m0, false)) return -4;
   auto kern = k_fp8_gemm<BN, GU>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGemmSmem(BN)) != cudaSuccess)
-    return -4;
+  static std::atomic<bool> checked{false};
+  if (!checked.load(std::memory_order_relaxed)) {
+    // the register split draws on what the launch takes: 5 x 96 for each lane of the five warpgroups
+    cudaFuncAttributes fa;
+    if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess) return -4;
+    if (fa.numRegs * (kGemmThreads / 128) != 4 * kEpiRegs + kLastRegs) return -3;
+    checked.store(true);
+  }
+  if (allow_smem<k_fp8_gemm<BN, GU>, kGemmSmem(BN)>()) return -4;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(tiles * split));
+  cfg.gridDim = dim3((unsigned)(split > 1 ? tiles * split : std::min<int64_t>(tiles, num_sms)));
   cfg.blockDim = dim3(kGemmThreads);
   cfg.dynamicSmemBytes = kGemmSmem(BN);
   cfg.stream = st;
   cudaLaunchAttribute at[2] = {pdl(), cluster_of(split)};
   cfg.attrs = at;
   cfg.numAttrs = split > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kern, mx, m0, m1, a, tiles_m, split) == cudaSuccess ? 0 : -4;
+  return cudaLaunchKernelEx(&cfg, kern, mx, m0, m1, a, tiles_m, (int)tiles, split) == cudaSuccess ? 0 : -4;
 }
 
 }  // namespace
@@ -634,9 +864,9 @@ int launch_fp8_quantize(const uint16_t* x, int64_t stride, int T, int cols, uint
 }
 
 int launch_fp8_product(const Fp8Args& a, bool gate_up, cudaStream_t st, int num_sms) {
-  if (a.T <= kGemvMaxT) {
-    if (gate_up) return a.T <= 8 ? launch_gemv_nt<1, true, 2>(a, st) : launch_gemv_nt<2, true, 1>(a, st);
-    return a.T <= 8 ? launch_gemv_nt<1, false, 4>(a, st) : launch_gemv_nt<2, false, 2>(a, st);
+  if (a.T <= kGemvMaxT && gemv_smem_bytes(a.T, a.nkb, kGemvWarps, a.T <= 8 ? 1 : 2, gate_up) <= kGemvSmemMax) {
+    if (gate_up) return a.T <= 8 ? launch_gemv_nt<1, true, 2>(a, st) : launch_gemv_nt<2, true, 2>(a, st);
+    return a.T <= 8 ? launch_gemv_nt<1, false, 4>(a, st) : launch_gemv_nt<2, false, 4>(a, st);
   }
   if (gate_up) return launch_gemm<256, true>(a, num_sms, st);
   const int64_t tiles = (int64_t)((a.T + kBM - 1) / kBM) * ((a.rows + 255) / 256);

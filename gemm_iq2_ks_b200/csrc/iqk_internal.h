@@ -163,6 +163,7 @@ struct TopkArgs {
   bool sigmoid, renorm;
   // set by launch_topk
   int32_t group_size, lanes_per_group, smem_row;
+  FastDiv by_group;
 };
 int launch_topk(TopkArgs a, bool bf16, cudaStream_t st);
 
@@ -184,6 +185,7 @@ struct Fp8Args {
   float* hs;          // gate_up: scales [T][ceil(rows / 128)]
   int32_t T, rows, cols, nkb;
   bool f32;
+  bool vec;  // rows, y and add allow accesses of four elements
 };
 int launch_fp8_product(const Fp8Args& a, bool gate_up, cudaStream_t st, int num_sms);
 // Whether a bounded wait of a product expired since the last call (cleared), after syncing `st`.
