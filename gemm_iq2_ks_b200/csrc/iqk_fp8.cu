@@ -50,31 +50,40 @@ __device__ __forceinline__ float snap18(float t) {
 }
 
 constexpr int kQuantThreads = 256;
-constexpr int kQuantUnroll = 4;
+constexpr int kQuantUnroll = 2;
+constexpr int kQuantBlocks = 5;  // resident on an SM
 
-// 16 lanes take one group of 128 columns, 8 columns (16 bytes) each.
-__global__ void __launch_bounds__(kQuantThreads) k_fp8_quantize(const uint16_t* x, int64_t stride, int cols,
-                                                                int nkb, FastDiv by_nkb, int items,
-                                                                uint8_t* q, float* s) {
+// 16 lanes take one group of 128 columns, 8 columns (16 bytes) each, two
+// groups at a time; the next two are on their way while these are converted.
+__global__ void __launch_bounds__(kQuantThreads, kQuantBlocks)
+    k_fp8_quantize(const uint16_t* x, int64_t stride, int cols, int nkb, FastDiv by_nkb, int items, uint8_t* q, float* s) {
   griddep_wait();
   griddep_launch();
   const int sub = threadIdx.x & 15;
   const int per = gridDim.x * (kQuantThreads / 16);
-  for (int it0 = blockIdx.x * (kQuantThreads / 16) + (threadIdx.x >> 4); it0 < items; it0 += per * kQuantUnroll) {
-    uint4 v[kQuantUnroll];
-    int row[kQuantUnroll], col[kQuantUnroll];
+  struct Group {
+    uint4 v;
+    int64_t at;  // offset of this lane's columns in q; negative: none
+  };
+  auto load = [&](Group (&g)[kQuantUnroll], int it0) {
 #pragma unroll
     for (int u = 0; u < kQuantUnroll; u++) {
       const int it = it0 + u * per;
-      row[u] = (int)by_nkb.div((uint32_t)it);
-      col[u] = (it - row[u] * nkb) * kFp8Block + sub * 8;
-      v[u] = make_uint4(0, 0, 0, 0);
-      if (it < items && col[u] < cols) v[u] = ld_u4(x + row[u] * stride + col[u]);
+      const int row = (int)by_nkb.div((uint32_t)it), col = (it - row * nkb) * kFp8Block + sub * 8;
+      const bool in = it < items && col < cols;
+      g[u].v = make_uint4(0, 0, 0, 0);
+      if (in) g[u].v = *reinterpret_cast<const uint4*>(x + row * stride + col);
+      g[u].at = in ? (int64_t)row * cols + col : -1;
     }
+  };
+  int it0 = blockIdx.x * (kQuantThreads / 16) + (threadIdx.x >> 4);
+  Group cur[kQuantUnroll], next[kQuantUnroll];
+  load(cur, it0);
+  for (; __any_sync(0xffffffffu, it0 < items); it0 += per * kQuantUnroll) {
+    load(next, it0 + per * kQuantUnroll);
 #pragma unroll
     for (int u = 0; u < kQuantUnroll; u++) {
-      const int it = it0 + u * per;
-      const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+      const uint32_t w[4] = {cur[u].v.x, cur[u].v.y, cur[u].v.z, cur[u].v.w};
       uint32_t m2 = 0;
 #pragma unroll
       for (int j = 0; j < 4; j++) m2 = __vmaxu2(m2, w[j] & 0x7fff7fffu);
@@ -94,10 +103,11 @@ __global__ void __launch_bounds__(kQuantThreads) k_fp8_quantize(const uint16_t* 
       o.x = e4m3x4(t[0], t[1], t[2], t[3]);
       o.y = e4m3x4(t[4], t[5], t[6], t[7]);
       if (!fine) o = make_uint2(0, 0);
-      if (it < items && col[u] < cols) {
-        *reinterpret_cast<uint2*>(q + (int64_t)row[u] * cols + col[u]) = o;
-        if (sub == 0) s[it] = fine ? most / kE4m3Max : __int_as_float(0x7fffffff);
+      if (cur[u].at >= 0) {
+        *reinterpret_cast<uint2*>(q + cur[u].at) = o;
+        if (sub == 0) s[it0 + u * per] = fine ? most / kE4m3Max : __int_as_float(0x7fffffff);
       }
+      cur[u] = next[u];
     }
   }
 }
@@ -851,7 +861,7 @@ int launch_fp8_quantize(const uint16_t* x, int64_t stride, int T, int cols, uint
   const int nkb = fp8_blocks(cols), items = T * nkb;
   const int per = kQuantThreads / 16;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)std::min((items + per - 1) / per, num_sms * 8));
+  cfg.gridDim = dim3((unsigned)std::min((items + per - 1) / per, num_sms * kQuantBlocks));
   cfg.blockDim = dim3(kQuantThreads);
   cfg.stream = st;
   cudaLaunchAttribute at[1] = {pdl()};

@@ -162,7 +162,7 @@ struct TopkArgs {
   float scale;
   bool sigmoid, renorm;
   // set by launch_topk
-  int32_t group_size, lanes_per_group, smem_row;
+  int32_t group_size, lanes_per_group, lanes_log2, smem_row, seg, seg_log2;
   FastDiv by_group;
 };
 int launch_topk(TopkArgs a, bool bf16, cudaStream_t st);

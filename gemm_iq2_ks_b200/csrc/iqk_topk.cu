@@ -102,41 +102,62 @@ __device__ __forceinline__ R score_of(float x, const Norm<R>& n, bool sigmoid) {
   return (v == n.most ? R(1) : exp_r(v - n.most)) / n.total;
 }
 
-// Selection value of expert e; -inf where it is masked.
-template <typename R>
-__device__ __forceinline__ R value_at(const TopkArgs& A, const Norm<R>& n, int e, float x) {
-  if (!A.bias) return (R)x;
-  const float b = A.bias[e];
-  if (x == -topk_inf() || !(b > -topk_inf())) return (R)-topk_inf();
-  return score_of<R>(x, n, A.sigmoid) + (R)b + R(0);  // never -0
+// The float32 score that selects: hardware exponential and reciprocal, without
+// branches (score_bound below bounds its error).
+__device__ __forceinline__ float quick_score(float x, const Norm<float>& n, bool sigmoid) {
+  if (sigmoid) {
+    const float e = __expf(-fabsf(x)), r = __fdividef(1.f, 1.f + e);
+    return x >= 0.f ? r : e * r;
+  }
+  return (x == n.most ? 1.f : __expf(x - n.most)) * n.total;  // total: its reciprocal here
+}
+template <int NV>
+__device__ __forceinline__ Norm<float> quick_norm(const float (&x)[NV], float most) {
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < NV; i++) s += x[i] == most ? 1.f : x[i] > -topk_inf() ? __expf(x[i] - most) : 0.f;
+  return {most, __fdividef(1.f, warp_sum(s))};
+}
+// exp(-d) by the hardware is within (1.5 d + 5) 2^-24 of itself and d exp(-d)
+// at most 0.37; sum, reciprocal and product add 2^-24 to 2^-23 each. A sigmoid
+// is then within 2^-21; a softmax within (NV + 24) 2^-24 of the largest score,
+// each of the NV + 5 additions of its sum another 2^-24.
+template <int NV>
+__device__ __forceinline__ float score_bound(const Norm<float>& n, bool sigmoid) {
+  return sigmoid ? 0x1p-21f : (NV + 24) * 0x1p-24f * fminf(n.total, 1.f);
 }
 
-// The open groups: bit g * lanes_per_group for each. v: the lane's selection
-// values, x its logits. L lanes take a group, each a strided part of it from
-// the values in shared memory; then the group's best two meet by shuffles.
+// Selection value of an expert with logit x and bias b; -inf where it is masked.
+__device__ __forceinline__ double value_of_expert(const Norm<double>& n, bool sigmoid, float x, float b) {
+  if (x == -topk_inf() || !(b > -topk_inf())) return -(double)topk_inf();
+  return score_of<double>(x, n, sigmoid) + (double)b + 0.0;  // never -0
+}
+__device__ __forceinline__ float value_of_expert(const Norm<float>& n, bool sigmoid, float x, float b) {
+  const float v = quick_score(x, n, sigmoid) + b + 0.f;
+  return x == -topk_inf() || !(b > -topk_inf()) ? -topk_inf() : v;
+}
+
+// The open groups of a row: bit g * lanes_per_group for each. v: the lane's
+// selection values. L lanes take a group, each a strided part of it from the
+// values in shared memory; then the group's best two meet by shuffles.
 // near: whether the last open group's value is within `margin` (and 2^-20 of
 // its size) of the first closed one's.
 template <typename R, int NV, int VEC>
-__device__ __forceinline__ unsigned open_groups(const TopkArgs& A, const R (&v)[NV], const float (&x)[NV], int lane,
-                                                const Norm<R>& norm, float margin, bool& near) {
+__device__ __forceinline__ unsigned open_groups(const TopkArgs& A, const R (&v)[NV], int lane, float margin, bool& near) {
   extern __shared__ __align__(16) unsigned char topk_smem[];
   R* row = reinterpret_cast<R*>(topk_smem) + (size_t)(threadIdx.x >> 5) * A.smem_row;
   const float inf = topk_inf();
-  const bool sums = A.group_top == 2;
   __syncwarp();
 #pragma unroll
   for (int i = 0; i < NV; i++) {
     const int e = expert_at<VEC>(i, lane);
-    if (e < A.experts) {
-      const R w = sums && !A.bias && x[i] != -inf ? score_of<R>(x[i], norm, A.sigmoid) : v[i];
-      row[e + (int)A.by_group.div((uint32_t)e)] = w;  // a value of padding per group spreads them over the banks
-    }
+    if (e < A.experts) row[e + (int)A.by_group.div((uint32_t)e)] = v[i];  // padded, to spread groups over the banks
   }
   __syncwarp();
-  const int L = A.lanes_per_group, g = lane / L;
+  const int L = A.lanes_per_group, g = lane >> A.lanes_log2;  // L: a power of two
   R b1 = (R)-inf, b2 = (R)-inf;
   if (g < A.groups)
-    for (int j = lane % L; j < A.group_size; j += L) {
+    for (int j = lane & (L - 1); j < A.group_size; j += L) {
       const R w = row[g * (A.group_size + 1) + j];
       const R lo = w < b1 ? w : b1;
       b1 = w < b1 ? b1 : w;
@@ -149,7 +170,7 @@ __device__ __forceinline__ unsigned open_groups(const TopkArgs& A, const R (&v)[
     b2 = b2 < o2 ? o2 : b2;
     b2 = b2 < lo ? lo : b2;
   }
-  const R val = b1 + (sums && b2 > (R)-inf ? b2 : R(0));
+  const R val = b1 + (A.group_top == 2 && b2 > (R)-inf ? b2 : R(0));
   int ahead = 0;
   for (int h = 0; h < A.groups; h++) {
     const R o = __shfl_sync(kFull, val, h * L);
@@ -171,6 +192,58 @@ __device__ __forceinline__ void close_groups(const TopkArgs& A, unsigned open, i
   for (int i = 0; i < NV; i++) {
     const int e = expert_at<VEC>(i, lane);
     if (e < A.experts && !((open >> ((int)A.by_group.div((uint32_t)e) * A.lanes_per_group)) & 1u)) key[i] = 0;
+  }
+}
+
+// The same in registers, where `seg` (a power of two) neighbouring lanes hold a
+// group: closes the other groups' keys.
+template <int NV, int VEC>
+__device__ __forceinline__ void close_groups_in_lanes(const TopkArgs& A, const float (&v)[NV], int lane, float margin,
+                                                      uint32_t (&key)[NV], bool& near) {
+  constexpr int C = NV / VEC;
+  const float inf = topk_inf();
+  const int seg = A.seg, per = 32 >> A.seg_log2;  // groups in a chunk of 32 * VEC experts
+  const int mine = lane >> A.seg_log2;
+  float val[C];
+  int ahead[C];
+#pragma unroll
+  for (int c = 0; c < C; c++) {
+    float b1 = -inf, b2 = -inf;
+#pragma unroll
+    for (int j = 0; j < VEC; j++) {
+      const float w = fmaxf(v[c * VEC + j], -inf);  // what is past the row's end counts as masked
+      b2 = fmaxf(b2, fminf(b1, w));
+      b1 = fmaxf(b1, w);
+    }
+    for (int d = 1; d < seg; d <<= 1) {
+      const float o1 = __shfl_xor_sync(kFull, b1, d), o2 = __shfl_xor_sync(kFull, b2, d);
+      b2 = fmaxf(fmaxf(b2, o2), fminf(b1, o1));
+      b1 = fmaxf(b1, o1);
+    }
+    val[c] = b1 + (A.group_top == 2 && b2 > -inf ? b2 : 0.f);
+    ahead[c] = 0;
+  }
+#pragma unroll
+  for (int c2 = 0; c2 < C; c2++)
+    for (int i = 0; i < per; i++) {
+      const float o = __shfl_sync(kFull, val[c2], i * seg);
+      const int h = c2 * per + i;
+#pragma unroll
+      for (int c = 0; c < C; c++)
+        ahead[c] += h < A.groups && (o > val[c] || (o == val[c] && h < c * per + mine)) ? 1 : 0;
+    }
+  uint32_t low = 0, high = kKeyNegInf;
+#pragma unroll
+  for (int c = 0; c < C; c++) {
+    const bool exists = c * per + mine < A.groups, in = exists && ahead[c] < A.topk_groups;
+    if (in) low = max(low, ~key_of(val[c]));
+    if (exists && !in) high = max(high, key_of(val[c]));
+#pragma unroll
+    for (int j = 0; j < VEC; j++) key[c * VEC + j] = in ? key[c * VEC + j] : 0u;
+  }
+  if (margin > 0.f && A.topk_groups < A.groups) {
+    const float least = value_of(~warp_max(low)), most = value_of(warp_max(high));
+    near = most > -inf && !(least - most > margin + 0x1p-20f * fmaxf(fabsf(least), fabsf(most)));
   }
 }
 
@@ -200,17 +273,22 @@ __device__ __noinline__ int select_row(const TopkArgs& A, const char* logits, in
   }
   const Norm<R> norm = norm_of<R, NV>(x, most, sizeof(R) == 8 && !A.sigmoid);
   R v[NV];
+  K key[NV];
 #pragma unroll
   for (int i = 0; i < NV; i++) {
     const int e = expert_at<VEC>(i, lane);
-    v[i] = e < A.experts ? value_at<R>(A, norm, e, x[i]) : (R)-topk_inf();
+    v[i] = (R)x[i];
+    if (A.bias && e < A.experts) v[i] = value_of_expert(norm, A.sigmoid, x[i], A.bias[e]);
+    key[i] = e < A.experts ? key_of(v[i]) : K(0);
   }
-  K key[NV];
-#pragma unroll
-  for (int i = 0; i < NV; i++) key[i] = expert_at<VEC>(i, lane) < A.experts ? key_of(v[i]) : K(0);
   if (A.groups > 1) {
+    if (A.group_top == 2 && !A.bias) {
+#pragma unroll
+      for (int i = 0; i < NV; i++)
+        if (x[i] != -topk_inf()) v[i] = score_of<R>(x[i], norm, A.sigmoid);
+    }
     bool near = false;
-    const unsigned open = open_groups<R, NV, VEC>(A, v, x, lane, norm, 0.f, near);
+    const unsigned open = open_groups<R, NV, VEC>(A, v, lane, 0.f, near);
     close_groups<NV, VEC>(A, open, lane, key);
   }
   int mine = 0;
@@ -234,7 +312,86 @@ __device__ __noinline__ int select_row(const TopkArgs& A, const char* logits, in
   return mine;
 }
 
+// Orders the n candidates (lane j < n has expert e, in roughly descending
+// order; every expert left out is certainly behind the topk best of them):
+// by exact logits, or by float32 scores if those are far enough apart, else by
+// float64 ones. Returns lane j's expert for j < topk.
 template <int NV, int VEC, bool BF16>
+__device__ __noinline__ int order_candidates(const TopkArgs& A, const char* logits, int lane, int e, int n, float most,
+                                             float total, float eps) {
+  const float inf = topk_inf();
+  const bool cand = lane < n;
+  const float x = cand ? clean(logit_at<BF16>(logits, e)) : -inf;
+  const float b = A.bias && cand ? A.bias[e] : 0.f;
+  int src = 0;
+  // lane r's source: the candidate with r others ahead of it
+  auto place = [&](auto v) {
+    int ahead = 0;
+    for (int h = 0; h < n; h++) {
+      const auto o = __shfl_sync(kFull, v, h);
+      const int oe = __shfl_sync(kFull, e, h);
+      ahead += (o > v || (o == v && oe < e)) ? 1 : 0;
+    }
+    for (int r = 0; r < min(n, A.topk + 1); r++) {
+      const unsigned at = __ballot_sync(kFull, cand && ahead == r);
+      if (lane == r) src = __ffs(at) - 1;
+    }
+  };
+  if (!A.bias) {
+    place(x);
+  } else {
+    const float v = cand ? value_of_expert(Norm<float>{most, total}, A.sigmoid, x, b) : -inf;
+    place(v);
+    const float here = __shfl_sync(kFull, v, src), next = __shfl_down_sync(kFull, here, 1);
+    const bool near = lane < A.topk && lane + 1 < n && next > -inf &&
+                      !(here - next > 2.f * (eps + 0x1p-23f * fmaxf(fabsf(here), fabsf(next))));
+    if (__any_sync(kFull, near)) {
+      Norm<double> norm{(double)most, 1.0};
+      if (!A.sigmoid) {
+        float xs[NV];
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+          const int j = expert_at<VEC>(i, lane);
+          xs[i] = j < A.experts ? clean(logit_at<BF16>(logits, j)) : -inf;
+        }
+        norm = norm_of<double, NV>(xs, most, true);
+      }
+      place(cand ? value_of_expert(norm, A.sigmoid, x, b) : -(double)inf);
+    }
+  }
+  return __shfl_sync(kFull, e, src);
+}
+
+// The two best of a lane's keys (those below `bound`).
+template <int NV>
+__device__ __forceinline__ void two_best(const uint32_t (&key)[NV], uint32_t bound, uint32_t& h1, uint32_t& h2) {
+  uint32_t a[NV], b[NV];
+#pragma unroll
+  for (int i = 0; i < NV; i++) a[i] = key[i] < bound ? key[i] : 0u;
+  if (NV == 1) {
+    h1 = a[0];
+    h2 = 0;
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < NV / 2; i++) {
+    b[i] = min(a[i], a[i + NV / 2]);
+    a[i] = max(a[i], a[i + NV / 2]);
+  }
+#pragma unroll
+  for (int n = NV / 4; n >= 1; n /= 2)
+#pragma unroll
+    for (int i = 0; i < n; i++) {
+      b[i] = max(max(b[i], b[i + n]), min(a[i], a[i + n]));
+      a[i] = max(a[i], a[i + n]);
+    }
+  h1 = a[0];
+  h2 = b[0];
+}
+
+// PLAIN: no bias, no groups, renormalised weights; scores are then needed for
+// the selected experts alone.
+template <int NV, int VEC, bool BF16, bool PLAIN>
 __global__ void __launch_bounds__(kTopkWarps * 32, NV <= 8 ? 4 : NV == 16 ? 2 : 1) k_topk(const __grid_constant__ TopkArgs A) {
   griddep_wait();
   griddep_launch();
@@ -243,124 +400,172 @@ __global__ void __launch_bounds__(kTopkWarps * 32, NV <= 8 ? 4 : NV == 16 ? 2 : 
   if (t >= A.T) return;
   const char* logits = static_cast<const char*>(A.logits) + t * A.stride * (BF16 ? 2 : 4);
   const float inf = topk_inf();
+  const float none = __uint_as_float(0xffffffffu);  // past the row's end: the key below all others
   float x[NV];
 #pragma unroll
   for (int c = 0; c < NV / VEC; c++) {
     const int e0 = expert_at<VEC>(c * VEC, lane);
-    if (VEC > 1 && e0 < A.experts) {  // experts is a multiple of VEC here, rows 16-byte aligned
-      const uint4 q = ld_u4(logits + (size_t)e0 * (BF16 ? 2 : 4));
-      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    if (VEC > 1) {  // experts is a multiple of VEC here, rows 16-byte aligned
+      if (e0 < A.experts) {
+        const uint4 q = ld_u4(logits + (size_t)e0 * (BF16 ? 2 : 4));
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-      for (int j = 0; j < VEC; j++) {
-        const uint32_t u = w[(BF16 ? j / 2 : j) & 3];
-        x[c * VEC + j] = clean(__uint_as_float(!BF16 ? u : (j & 1) ? (u & 0xffff0000u) : (u << 16)));
+        for (int j = 0; j < VEC; j++) {
+          const uint32_t u = w[(BF16 ? j / 2 : j) & 3];
+          x[c * VEC + j] = clean(__uint_as_float(!BF16 ? u : (j & 1) ? (u & 0xffff0000u) : (u << 16)));
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < VEC; j++) x[c * VEC + j] = none;
       }
     } else {
-#pragma unroll
-      for (int j = 0; j < VEC; j++)
-        x[c * VEC + j] = e0 + j < A.experts ? clean(logit_at<BF16>(logits, e0 + j)) : -inf;
+      x[c] = e0 < A.experts ? clean(logit_at<BF16>(logits, e0)) : none;
     }
   }
   // softmax needs the row's maximum, and its sum where scores themselves count
-  const bool scored = A.bias != nullptr;
-  const bool scores = scored || (A.groups > 1 && A.group_top == 2);
-  const bool sum = !A.sigmoid && (scores || !A.renorm);
+  const bool scored = !PLAIN && A.bias != nullptr;
+  float bias[NV];
+  if (scored) {
+#pragma unroll
+    for (int i = 0; i < NV; i += VEC > 1 ? 4 : 1) {
+      const int e = expert_at<VEC>(i, lane);
+      if constexpr (VEC > 1) {
+        const uint4 q = e < A.experts ? ld_u4(A.bias + e) : make_uint4(0, 0, 0, 0);
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int j = 0; j < 4; j++) bias[i + j] = __uint_as_float(w[j]);
+      } else {
+        bias[i] = e < A.experts ? A.bias[e] : 0.f;
+      }
+    }
+  }
+  const bool scores = !PLAIN && (scored || (A.groups > 1 && A.group_top == 2));
+  const bool sum = !PLAIN && !A.sigmoid && (scores || !A.renorm);
   float most = 0.f;
   if (sum) {
-    most = x[0];
+    most = -inf;
 #pragma unroll
-    for (int i = 1; i < NV; i++) most = fmaxf(most, x[i]);
+    for (int i = 0; i < NV; i++) most = fmaxf(most, x[i]);  // `none` is a NaN, which fmaxf passes over
     most = value_of(warp_max(key_of(most)));
   }
-  const Norm<float> norm = norm_of<float, NV>(x, most, sum);
-  // Bound of float32's error in a score: a few ulp of the largest one, plus
-  // 2^-24 for each of the NV + 5 additions of a softmax sum; for a sigmoid
-  // s (1 - s) 2^-22 from the exponential and 2^-23 from sum and quotient.
-  const float eps = !scores ? 0.f : A.sigmoid ? 0x1p-22f : (NV + 16) * 0x1p-24f / fmaxf(norm.total, 1.f);
+  Norm<float> norm{most, 1.f};
+  if (sum) norm = quick_norm<NV>(x, most);
+  const float eps = scores ? score_bound<NV>(norm, A.sigmoid) : 0.f;
 
   // Packed keys: the leading bits of the value's key, then the index, inverted
   // so that ties go to the lowest. bf16 logits fit whole; of a float32 value
-  // the bits that give way to the index are lost, and neighbours that then
-  // look alike (or lie within the scores' error) send the row to select_row.
+  // the bits that give way to the index are lost, and where neighbours then
+  // look alike (or lie within the scores' error) the candidates are ordered
+  // anew from whole values.
   constexpr uint32_t kMask = 32u * NV - 1;
   const bool whole = BF16 && !scored;
   const uint32_t cut = whole ? 0xffffu : kMask;
   uint32_t key[NV];
   bool near = false;
-  {
-    float v[NV];
+  if (scored) {
 #pragma unroll
-    for (int i = 0; i < NV; i++) {
-      const int e = expert_at<VEC>(i, lane);
-      v[i] = scored && e < A.experts ? value_at<float>(A, norm, e, x[i]) : x[i];
-      key[i] = e < A.experts ? (key_of(v[i]) & ~cut) | (kMask - (uint32_t)e) : 0u;
+    for (int i = 0; i < NV; i++)
+      x[i] = expert_at<VEC>(i, lane) < A.experts ? value_of_expert(norm, A.sigmoid, x[i], bias[i]) : none;
+  }
+#pragma unroll
+  for (int i = 0; i < NV; i++) key[i] = (key_of(x[i]) & ~cut) | (kMask - (uint32_t)expert_at<VEC>(i, lane));
+  if (!PLAIN && A.groups > 1) {
+    if (scores && !scored) {
+#pragma unroll
+      for (int i = 0; i < NV; i++)
+        if (x[i] != -inf) x[i] = quick_score(x[i], norm, A.sigmoid);
     }
-    if (A.groups > 1) {
-      const unsigned open = open_groups<float, NV, VEC>(A, v, x, lane, norm, 4.f * eps, near);
+    bool done = false;
+    if constexpr (VEC > 1) {
+      if (A.seg) {
+        close_groups_in_lanes<NV, VEC>(A, x, lane, 4.f * eps, key, near);
+        done = true;
+      }
+    }
+    if (!done) {
+      const unsigned open = open_groups<float, NV, VEC>(A, x, lane, 4.f * eps, near);
       close_groups<NV, VEC>(A, open, lane, key);
     }
   }
-  // Each lane keeps its two best; a maximum over the warp takes one expert.
-  uint32_t h1 = 0, h2 = 0;
-  auto two_below = [&](uint32_t bound) {
-    h1 = 0;
-    h2 = 0;
-#pragma unroll
-    for (int i = 0; i < NV; i++) {
-      const uint32_t k = key[i] < bound ? key[i] : 0u;
-      h2 = max(h2, min(h1, k));
-      h1 = max(h1, k);
+  // Each lane keeps its two best; a maximum over the warp takes one expert. A
+  // lane whose two are taken shows kRefill, above all keys, and the warp then
+  // fetches its next two.
+  constexpr uint32_t kRefill = 0xffffffffu;
+  uint32_t h1, h2, taken = 0, got = 0;
+  two_best<NV>(key, kRefill, h1, h2);
+  auto take = [&](int j) {
+    uint32_t top = warp_max(h1);
+    if (NV > 1 && top == kRefill) {
+      if (h1 == kRefill) two_best<NV>(key, taken, h1, h2);
+      top = warp_max(h1);
     }
-  };
-  two_below(0xffffffffu);
-  uint32_t got = 0;
-  const int rounds = whole ? A.topk : A.topk + 1;  // the best one left out, too
-  for (int j = 0; j < rounds; j++) {
-    const uint32_t top = warp_max(h1);
     if (lane == j) got = top;
-    const bool mine = h1 == top;
-    if (mine) {
+    if (h1 == top) {
       h1 = h2;
-      h2 = 0;
+      h2 = NV > 2 ? kRefill : 0u;
+      taken = top;
     }
-    if (NV > 2 && __any_sync(kFull, mine && h1 == 0 && top != 0)) {
-      if (mine) two_below(top);
-    }
-  }
+    return top;
+  };
+  uint32_t kth = 0;
+  for (int j = 0; j < A.topk; j++) kth = take(j);
+  int mine = (int)(kMask - (got & cut));
+  bool whole_row = !PLAIN && near;  // the groups are in doubt
   if (!whole) {
-    const uint32_t next = __shfl_down_sync(kFull, got, 1);
-    // masked values share one key and are in order; so is the end of the open experts
-    if (lane < A.topk && (next & ~cut) != (kKeyNegInf & ~cut) && next != 0) {
-      if (!scored) {
-        near = near || (got & ~cut) == (next & ~cut);
-      } else {
-        const float lo = value_of(got & ~cut), hi = value_of(next | cut);
-        near = near || !(lo - hi > 2.f * (eps + 0x1p-23f * fmaxf(fabsf(lo), fabsf(hi))));
+    // Further candidates, until the next is certainly behind the last selected
+    // one; masked values share one key, are in order, and nothing follows them.
+    const float lo = value_of(kth & ~cut);
+    int n = A.topk;
+    if ((kth & ~cut) > (kKeyNegInf & ~cut)) {
+      for (;;) {
+        const uint32_t top = take(n & 31);
+        if ((top & ~cut) <= (kKeyNegInf & ~cut)) break;
+        const float hi = value_of(top | cut);
+        if (!scored ? (top & ~cut) != (kth & ~cut)
+                    : lo - hi > 2.f * (eps + 0x1p-23f * fmaxf(fabsf(lo), fabsf(hi))) || (lo == inf && hi < inf))
+          break;
+        if (++n > 31) break;
       }
     }
+    whole_row = whole_row || n > 31;
+    const uint32_t next = __shfl_down_sync(kFull, got, 1);
+    bool alike = false;
+    if (lane + 1 < n && (next & ~cut) > (kKeyNegInf & ~cut)) {
+      const float l = value_of(got & ~cut), h = value_of(next | cut);
+      alike = !scored ? (got & ~cut) == (next & ~cut)
+                      : !(l - h > 2.f * (eps + 0x1p-23f * fmaxf(fabsf(l), fabsf(h))));
+    }
+    mine = (int)(kMask - (got & cut));
+    if (!whole_row && __any_sync(kFull, alike))
+      mine = order_candidates<NV, VEC, BF16>(A, logits, lane, mine, n, norm.most, norm.total, eps);
   }
-  int mine = (int)(kMask - (got & cut));
-  if (__any_sync(kFull, near))
+  if (whole_row)
     mine = scores ? select_row<double, NV, VEC, BF16>(A, logits, lane, most)
                   : select_row<float, NV, VEC, BF16>(A, logits, lane, most);
 
   // weights: lane j has expert j
   const bool have = lane < A.topk;
-  float xm = have ? clean(logit_at<BF16>(logits, mine)) : -inf;
-  if (have && scored && !(A.bias[mine] > -inf)) xm = -inf;
+  float xm = -inf;
+  if (PLAIN && BF16)
+    xm = have ? __uint_as_float(__float_as_uint(value_of(got)) & 0xffff0000u) : -inf;  // the key's bf16 half
+  else if (have && (!scored || A.bias[mine] > -inf))
+    xm = clean(logit_at<BF16>(logits, mine));
   float w;
-  if (!A.renorm) {
-    w = score_of<float>(xm, norm, A.sigmoid);
+  if (!PLAIN && !A.renorm) {
+    w = xm == -inf ? 0.f
+        : A.sigmoid ? score_of<float>(xm, norm, true)
+                    : (xm == norm.most ? 1.f : expf(xm - norm.most)) * norm.total;
   } else {
     // relative to the largest selected logit, so that small scores keep their ratios
-    const float ms = value_of(warp_max(key_of(xm)));
-    if (xm == -inf)
-      w = 0.f;
-    else if (!A.sigmoid)
+    const float ms = PLAIN ? __shfl_sync(kFull, xm, 0) : value_of(warp_max(key_of(xm)));
+    if (!A.sigmoid)
       w = xm == ms ? 1.f : expf(xm - ms);
     else
       w = xm >= 0.f ? 1.f / (1.f + expf(-xm)) : expf(xm - fminf(ms, 0.f)) / (1.f + expf(xm));
-    const float total = warp_sum(w);
+    if (xm == -inf) w = 0.f;
+    float total = w;  // of the first 16 lanes
+#pragma unroll
+    for (int d = 8; d; d >>= 1) total += __shfl_xor_sync(kFull, total, d);
     w = total > 0.f ? w / total : 0.f;
   }
   if (have) {
@@ -382,12 +587,21 @@ int launch_nv(const TopkArgs& a, int vec, bool bf16, cudaStream_t st) {
   cfg.attrs = at;
   cfg.numAttrs = 1;
   constexpr int V8 = NV >= 8 ? 8 : 1, V4 = NV >= 4 ? 4 : 1;
-  auto kern = bf16 ? (vec == 8 ? k_topk<NV, V8, true> : k_topk<NV, 1, true>)
-                   : (vec == 4 ? k_topk<NV, V4, false> : k_topk<NV, 1, false>);
+  const bool plain = !a.bias && a.groups == 1 && a.renorm;
+  auto kern = plain ? (bf16 ? (vec == 8 ? k_topk<NV, V8, true, true> : k_topk<NV, 1, true, true>)
+                            : (vec == 4 ? k_topk<NV, V4, false, true> : k_topk<NV, 1, false, true>))
+                    : (bf16 ? (vec == 8 ? k_topk<NV, V8, true, false> : k_topk<NV, 1, true, false>)
+                            : (vec == 4 ? k_topk<NV, V4, false, false> : k_topk<NV, 1, false, false>));
   if (cfg.dynamicSmemBytes > 48 * 1024 &&
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes) != cudaSuccess)
     return -4;
   return cudaLaunchKernelEx(&cfg, kern, a) == cudaSuccess ? 0 : -4;
+}
+
+int log2_of(int n) {
+  int l = 0;
+  while (n >> (l + 1)) l++;
+  return l;
 }
 
 }  // namespace
@@ -397,13 +611,19 @@ int launch_topk(TopkArgs a, bool bf16, cudaStream_t st) {
   int g2 = 1;
   while (g2 < a.groups) g2 *= 2;
   a.lanes_per_group = 32 / g2;
+  a.lanes_log2 = log2_of(a.lanes_per_group);
   a.smem_row = a.experts + a.groups;
   a.by_group = FastDiv::of((uint32_t)a.group_size);
   const int item = bf16 ? 2 : 4, per = 16 / item;
-  const bool wide = reinterpret_cast<uintptr_t>(a.logits) % 16 == 0 && a.stride % per == 0 && a.experts % per == 0;
+  const bool wide = reinterpret_cast<uintptr_t>(a.logits) % 16 == 0 && a.stride % per == 0 && a.experts % per == 0 &&
+                    reinterpret_cast<uintptr_t>(a.bias) % 16 == 0;
   int nv = 1;
   while (nv * 32 < a.experts) nv *= 2;
   const int vec = wide && nv >= per ? per : 1;
+  // groups held by a power of two of neighbouring lanes
+  const int seg = a.group_size / vec;
+  a.seg = vec > 1 && a.group_size % vec == 0 && seg <= 32 && (seg & (seg - 1)) == 0 ? seg : 0;
+  a.seg_log2 = log2_of(a.seg);
   switch (nv) {
     case 1: return launch_nv<1>(a, vec, bf16, st);
     case 2: return launch_nv<2>(a, vec, bf16, st);
