@@ -453,11 +453,6 @@ def iqk_set_wait_limit_ns(limit_ns: int, expire: bool = False) -> int:
 _SCORES = {"softmax": 0, "sigmoid": 1}
 
 
-def _need(ok: bool, what: str) -> None:
-    if not ok:
-        raise ValueError(what)
-
-
 def _dense(t, shape, dtype, device, what: str):
     """t, or a new tensor where it is None: a contiguous CUDA tensor of this shape, type and device."""
     if t is None:
@@ -468,23 +463,26 @@ def _dense(t, shape, dtype, device, what: str):
                      f"{list(t.shape)} on {t.device}")
 
 
-def _rows(t, what: str):
-    """Shape and row stride of a CUDA matrix whose rows are contiguous."""
-    _need(t.is_cuda and t.dim() == 2, f"{what} must be a CUDA tensor of two dimensions")
-    T, n = t.shape
+def _row_stride(t, what: str) -> int:
+    """Row stride of a CUDA matrix whose rows are contiguous."""
+    if not t.is_cuda or t.dim() != 2:
+        raise ValueError(f"{what} must be a CUDA tensor of two dimensions")
     stride, one = t.stride()
-    _need(one == 1 or n == 1 or T == 0, f"{what} must have contiguous rows")
-    return T, n, stride if T > 1 else n
+    T, n = t.shape
+    if one != 1 and n > 1 and T > 0:
+        raise ValueError(f"{what} must have contiguous rows")
+    return stride if T > 1 else n
 
 
 def _launch(fn, what: str, device, stream, *args) -> None:
     """Call an entry point on the tensors' device."""
-    C = _torch()._C
-    at = device.index
+    torch = _torch()
+    C, at = torch._C, device.index
     if C._cuda_getDevice() != at:
-        with _torch().cuda.device(at):
-            return _launch(fn, what, device, stream, *args)
-    rc = fn(*args, C._cuda_getCurrentRawStream(at) if stream is None else stream.cuda_stream)
+        with torch.cuda.device(at):
+            rc = fn(*args, C._cuda_getCurrentRawStream(at) if stream is None else stream.cuda_stream)
+    else:
+        rc = fn(*args, C._cuda_getCurrentRawStream(at) if stream is None else stream.cuda_stream)
     if rc:
         _check(rc, what)
 
@@ -495,18 +493,21 @@ def iqk_moe_topk(logits, topk: int, score: str = "softmax", bias=None, groups: i
     (float32 or bfloat16, rows may be strided): (ids int32 [T, topk], p float32
     [T, topk]), what iqk_moe_decode and iqk_moe_prefill take."""
     torch = _torch()
-    T, E, stride = _rows(logits, "logits")
+    stride = _row_stride(logits, "logits")
+    T, E = logits.shape
     dev, dt = logits.device, logits.dtype
-    _need(dt is torch.float32 or dt is torch.bfloat16, "logits must be float32 or bfloat16")
-    _need(score in _SCORES, f"unknown score {score!r} (expected one of {sorted(_SCORES)})")
-    if bias is not None:
-        _dense(bias, (E,), torch.float32, dev, "bias")
+    bf16 = dt is torch.bfloat16
+    if not bf16 and dt is not torch.float32:
+        raise ValueError("logits must be float32 or bfloat16")
+    kind = _SCORES.get(score)
+    if kind is None:
+        raise ValueError(f"unknown score {score!r} (expected one of {sorted(_SCORES)})")
     shape = (T, topk)
     ids = _dense(ids, shape, torch.int32, dev, "ids")
     p = _dense(p, shape, torch.float32, dev, "p")
-    _launch(lib().iqk_moe_topk, "iqk_moe_topk", dev, stream, logits.data_ptr(), 0 if dt is torch.float32 else 1, stride,
-            T, E, topk, _SCORES[score], None if bias is None else bias.data_ptr(), groups, topk_groups, group_top,
-            1 if renorm else 0, scale, ids.data_ptr(), p.data_ptr())
+    _launch(lib().iqk_moe_topk, "iqk_moe_topk", dev, stream, logits.data_ptr(), 1 if bf16 else 0, stride, T, E, topk,
+            kind, None if bias is None else _dense(bias, (E,), torch.float32, dev, "bias").data_ptr(), groups,
+            topk_groups, group_top, 1 if renorm else 0, scale, ids.data_ptr(), p.data_ptr())
     return ids, p
 
 
@@ -514,24 +515,37 @@ def iqk_fp8_quantize(x, q=None, s=None, stream=None):
     """e4m3 codes and scales of bfloat16 x [T, cols] (rows may be strided), per
     row and 128 columns: (q float8_e4m3fn [T, cols], s float32 [T, ceil(cols / 128)])."""
     torch = _torch()
-    T, cols, stride = _rows(x, "x")
+    stride = _row_stride(x, "x")
+    T, cols = shape = x.shape
     dev = x.device
-    _need(x.dtype is torch.bfloat16, "x must be bfloat16")
-    q = _dense(q, (T, cols), torch.float8_e4m3fn, dev, "q")
-    s = _dense(s, (T, (cols + 127) // 128), torch.float32, dev, "s")
+    if x.dtype is not torch.bfloat16:
+        raise ValueError("x must be bfloat16")
+    q = _dense(q, shape, torch.float8_e4m3fn, dev, "q")
+    s = _dense(s, (T, (cols + 127) >> 7), torch.float32, dev, "s")
     _launch(lib().iqk_fp8_quantize, "iqk_fp8_quantize", dev, stream, x.data_ptr(), stride, T, cols, q.data_ptr(),
             s.data_ptr())
     return q, s
 
 
-def _fp8_operand(q, s, block_rows: int, device, what: str):
-    """(rows, cols) of e4m3 codes q with their scales s per block_rows x 128 block."""
-    _need(q.is_cuda and q.dim() == 2, f"{what} must be a CUDA tensor of two dimensions")
-    shape = rows, cols = q.shape
+def _fp8_operands(wq, ws, xq, xs) -> None:
+    """Check weights [rows, cols] with scales per 128 x 128 block and activations
+    [T, cols] with scales per row and 128 columns."""
     torch = _torch()
-    _dense(q, shape, torch.float8_e4m3fn, device, what)
-    _dense(s, ((rows + block_rows - 1) // block_rows, (cols + 127) // 128), torch.float32, device, "its scales")
-    return shape
+    f8, f32, dev = torch.float8_e4m3fn, torch.float32, wq.device
+    rows, cols = wq.shape
+    T, n = xq.shape
+    nkb = (cols + 127) >> 7
+    if (n == cols and wq.dtype is f8 and xq.dtype is f8 and ws.dtype is f32 and xs.dtype is f32 and wq.is_cuda
+            and xq.device == dev and ws.device == dev and xs.device == dev
+            and ws.shape == ((rows + 127) >> 7, nkb) and xs.shape == (T, nkb)
+            and wq.is_contiguous() and ws.is_contiguous() and xq.is_contiguous() and xs.is_contiguous()):
+        return
+    if not wq.is_cuda:
+        raise ValueError("weights must be CUDA tensors")
+    _dense(wq, (rows, cols), f8, dev, "the weights")
+    _dense(ws, ((rows + 127) >> 7, nkb), f32, dev, "the weights' scales")
+    _dense(xq, (T, cols), f8, dev, "xq")
+    _dense(xs, (T, nkb), f32, dev, "xs")
 
 
 def iqk_fp8_linear(wq, ws, xq, xs, add=None, y=None, dtype=None, stream=None):
@@ -540,20 +554,19 @@ def iqk_fp8_linear(wq, ws, xq, xs, add=None, y=None, dtype=None, stream=None):
     gives them. y is bfloat16 or float32 (`dtype`; by default y's or add's type,
     else bfloat16); add has y's type and may be y."""
     torch = _torch()
-    dev = wq.device
-    rows, cols = _fp8_operand(wq, ws, 128, dev, "wq")
-    T, xcols = _fp8_operand(xq, xs, 1, dev, "xq")
-    _need(xcols == cols, "xq must be [T, cols]")
+    _fp8_operands(wq, ws, xq, xs)
+    rows, cols = wq.shape
+    T, dev = xq.shape[0], wq.device
     if dtype is None:
         dtype = y.dtype if y is not None else add.dtype if add is not None else torch.bfloat16
-    _need(dtype is torch.bfloat16 or dtype is torch.float32, "y must be bfloat16 or float32")
+    bf16 = dtype is torch.bfloat16
+    if not bf16 and dtype is not torch.float32:
+        raise ValueError("y must be bfloat16 or float32")
     shape = (T, rows)
-    if add is not None:
-        _dense(add, shape, dtype, dev, "add")
     y = _dense(y, shape, dtype, dev, "y")
     _launch(lib().iqk_fp8_linear, "iqk_fp8_linear", dev, stream, wq.data_ptr(), ws.data_ptr(), rows, cols,
-            xq.data_ptr(), xs.data_ptr(), T, None if add is None else add.data_ptr(), y.data_ptr(),
-            1 if dtype is torch.bfloat16 else 0)
+            xq.data_ptr(), xs.data_ptr(), T,
+            None if add is None else _dense(add, shape, dtype, dev, "add").data_ptr(), y.data_ptr(), 1 if bf16 else 0)
     return y
 
 
@@ -562,13 +575,14 @@ def iqk_fp8_gate_up(gate_q, gate_s, up_q, up_s, xq, xs, q=None, s=None, stream=N
     [T, inter], s float32 [T, ceil(inter / 128)]), what iqk_fp8_linear takes as
     xq, xs for the down product."""
     torch = _torch()
-    dev = gate_q.device
-    shape = inter, cols = _fp8_operand(gate_q, gate_s, 128, dev, "gate_q")
-    _need(_fp8_operand(up_q, up_s, 128, dev, "up_q") == shape, "gate_q and up_q must have one shape")
-    T, xcols = _fp8_operand(xq, xs, 1, dev, "xq")
-    _need(xcols == cols, "xq must be [T, cols]")
-    q = _dense(q, (T, inter), torch.float8_e4m3fn, dev, "q")
-    s = _dense(s, (T, (inter + 127) // 128), torch.float32, dev, "s")
+    _fp8_operands(gate_q, gate_s, xq, xs)
+    inter, cols = shape = gate_q.shape
+    T, dev = xq.shape[0], gate_q.device
+    f8, f32 = torch.float8_e4m3fn, torch.float32
+    _dense(up_q, shape, f8, dev, "up_q")
+    _dense(up_s, gate_s.shape, f32, dev, "up_s")
+    q = _dense(q, (T, inter), f8, dev, "q")
+    s = _dense(s, (T, (inter + 127) >> 7), f32, dev, "s")
     _launch(lib().iqk_fp8_gate_up, "iqk_fp8_gate_up", dev, stream, gate_q.data_ptr(), gate_s.data_ptr(),
             up_q.data_ptr(), up_s.data_ptr(), inter, cols, xq.data_ptr(), xs.data_ptr(), T, q.data_ptr(),
             s.data_ptr())

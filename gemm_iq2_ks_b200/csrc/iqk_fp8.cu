@@ -112,21 +112,7 @@ __global__ void __launch_bounds__(kQuantThreads, kQuantBlocks)
   }
 }
 
-// ------------------------------------------------------------ few tokens
-//
-// Up to 16 tokens: a stream over the weights. A CTA takes 16 rows (16 gate and
-// 16 up rows), its warps the 128-column blocks in turn; each lane loads the
-// 16-byte pieces of its fragments straight from global memory (the k order
-// inside a 64-column chunk is the same permutation for both operands, so the
-// dot products are unchanged), all blocks of a round before the first use.
-
-__device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
+// ------------------------------------------------------------------ products
 
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -139,9 +125,6 @@ __device__ __forceinline__ uint32_t peer_smem(const void* p, uint32_t rank) {
   uint32_t r;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
   return r;
-}
-__device__ __forceinline__ void st_peer(uint32_t addr, float v) {
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 __device__ __forceinline__ float4 ld_peer4(uint32_t addr) {
   float4 v;
@@ -166,176 +149,6 @@ __device__ __forceinline__ void put_y(const Fp8Args& A, int64_t i, float v) {
 __device__ __forceinline__ float magnitude(float h) {  // infinity for what is not finite
   const float m = fabsf(h);
   return m <= 3.402823466e38f ? m : __int_as_float(0x7f800000);
-}
-
-constexpr int kGemvMaxT = 16;
-constexpr size_t kGemvSmemMax = 110 * 1024;  // two CTAs in an SM's shared memory; beyond it the tiles take the call
-constexpr int kGemvRows = 16;
-constexpr int kGemvWarps = 8;  // at most; two CTAs fit an SM, so the next call's can start under this one's
-constexpr int kGuCluster = kFp8Block / kGemvRows;  // CTAs whose rows make up one scale's 128 columns of h
-
-// Shared memory: x rows (pitch nkb * 128 + 64 bytes, so that two neighbouring
-// tokens' pieces fall into different banks), the scales of x and of the
-// weights' blocks, then the warps' sums.
-__host__ __device__ inline int gemv_pitch(int nkb) { return nkb * kFp8Block + 64; }
-__host__ __device__ inline size_t gemv_x_bytes(int T, int nkb, int mats) {
-  return ((size_t)T * gemv_pitch(nkb) + (size_t)(T + mats) * nkb * 4 + 15) / 16 * 16;
-}
-
-__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-}
-
-template <int NT, bool GU, int U>
-__global__ void __launch_bounds__(kGemvWarps * 32, NT == 1 ? 2 : 1) k_fp8_gemv(const __grid_constant__ Fp8Args A) {
-  constexpr int M = GU ? 2 : 1, TOK = 8 * NT;
-  extern __shared__ __align__(16) uint8_t gemv_smem[];
-  __shared__ float s_amax[kGuCluster][kGemvMaxT];
-  griddep_wait();
-  griddep_launch();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
-  const int g = lane >> 2, tq = lane & 3;
-  const int row0 = blockIdx.x * kGemvRows;
-  if (GU) cluster_arrive();  // every CTA of the cluster runs before its shared memory is written to
-  const int pitch = gemv_pitch(A.nkb);
-  uint8_t* s_x = gemv_smem;
-  float* s_xs = reinterpret_cast<float*>(gemv_smem + (size_t)A.T * pitch);  // [T][nkb]
-  float* s_ws = s_xs + A.T * A.nkb;                                         // [M][nkb]
-  float* s_sum = reinterpret_cast<float*>(gemv_smem + gemv_x_bytes(A.T, A.nkb, M));
-
-  // Rows past the end read the last one's data; what they give is not stored.
-  const int rb = min(row0, A.rows - 1);
-  const uint8_t* wp[M][2];
-#pragma unroll
-  for (int m = 0; m < M; m++)
-#pragma unroll
-    for (int r = 0; r < 2; r++)
-      wp[m][r] = (m ? A.w1.q : A.w0.q) + (int64_t)min(row0 + g + 8 * r, A.rows - 1) * A.cols + 16 * tq;
-  const int kleft = A.cols - 16 * tq;  // columns from this lane's first piece on
-  uint4 w[U][M][2][2];                 // U blocks in flight: [row g, g + 8][64-column chunk]
-  auto load = [&](int u, int kb) {
-#pragma unroll
-    for (int c = 0; c < 2; c++) {
-      const int k = kb * kFp8Block + 64 * c;
-      const bool in = k < kleft;  // false as well for kb past the last block
-#pragma unroll
-      for (int m = 0; m < M; m++)
-#pragma unroll
-        for (int r = 0; r < 2; r++) {
-          w[u][m][r][c] = make_uint4(0, 0, 0, 0);
-          if (in) w[u][m][r][c] = *reinterpret_cast<const uint4*>(wp[m][r] + k);
-        }
-    }
-  };
-#pragma unroll
-  for (int u = 0; u < U; u++) load(u, warp + u * nw);
-
-  // x and the scales, while the first weights are on their way
-  for (int t = 0; t < A.T; t++)
-    for (int k = threadIdx.x * 16; k < A.nkb * kFp8Block; k += blockDim.x * 16) {
-      if (k < A.cols)
-        cp_async16(s_x + t * pitch + k, A.xq + (int64_t)t * A.cols + k);
-      else
-        *reinterpret_cast<uint4*>(s_x + t * pitch + k) = make_uint4(0, 0, 0, 0);
-    }
-  for (int i = threadIdx.x; i < A.T * A.nkb; i += blockDim.x) s_xs[i] = A.xs[i];
-  for (int i = threadIdx.x; i < A.nkb; i += blockDim.x) {
-#pragma unroll
-    for (int m = 0; m < M; m++) s_ws[m * A.nkb + i] = (m ? A.w1.s : A.w0.s)[(int64_t)(rb / kFp8Block) * A.nkb + i];
-  }
-  asm volatile("cp.async.wait_all;" ::: "memory");
-  __syncthreads();
-
-  float acc[M][NT][4] = {};
-  const uint8_t* xr[NT];
-  int st[NT][2];
-#pragma unroll
-  for (int n = 0; n < NT; n++) {
-    xr[n] = s_x + min(8 * n + g, A.T - 1) * pitch + 16 * tq;
-#pragma unroll
-    for (int j = 0; j < 2; j++) st[n][j] = min(8 * n + 2 * tq + j, A.T - 1) * A.nkb;
-  }
-  for (int kb0 = warp; kb0 < A.nkb; kb0 += nw * U) {
-#pragma unroll
-    for (int u = 0; u < U; u++) {
-      const int kb = kb0 + u * nw;
-      if (kb >= A.nkb) break;
-#pragma unroll
-      for (int n = 0; n < NT; n++) {
-        const uint4 x0 = *reinterpret_cast<const uint4*>(xr[n] + kb * kFp8Block);
-        const uint4 x1 = *reinterpret_cast<const uint4*>(xr[n] + kb * kFp8Block + 64);
-        const float sx0 = s_xs[st[n][0] + kb], sx1 = s_xs[st[n][1] + kb];
-#pragma unroll
-        for (int m = 0; m < M; m++) {
-          float d[4] = {0.f, 0.f, 0.f, 0.f};
-          const uint4 a0 = w[u][m][0][0], b0 = w[u][m][1][0], a1 = w[u][m][0][1], b1 = w[u][m][1][1];
-          mma_e4m3(d, a0.x, b0.x, a0.y, b0.y, x0.x, x0.y);
-          mma_e4m3(d, a0.z, b0.z, a0.w, b0.w, x0.z, x0.w);
-          mma_e4m3(d, a1.x, b1.x, a1.y, b1.y, x1.x, x1.y);
-          mma_e4m3(d, a1.z, b1.z, a1.w, b1.w, x1.z, x1.w);
-          // d: (row g, tokens 2 tq, 2 tq + 1), (row g + 8, the same)
-          const float sw = s_ws[m * A.nkb + kb], s0 = sw * sx0, s1 = sw * sx1;
-          acc[m][n][0] += d[0] * s0;
-          acc[m][n][1] += d[1] * s1;
-          acc[m][n][2] += d[2] * s0;
-          acc[m][n][3] += d[3] * s1;
-        }
-      }
-      load(u, kb + U * nw);
-    }
-  }
-#pragma unroll
-  for (int m = 0; m < M; m++)
-#pragma unroll
-    for (int n = 0; n < NT; n++)
-#pragma unroll
-      for (int j = 0; j < 4; j++)
-        s_sum[((warp * M + m) * TOK + 8 * n + 2 * tq + (j & 1)) * kGemvRows + g + 8 * (j >> 1)] = acc[m][n][j];
-  __syncthreads();
-  // Warps' sums in order; 16 consecutive lanes hold one token's 16 rows.
-  if (!GU) {
-    for (int i = threadIdx.x; i < A.T * kGemvRows; i += blockDim.x) {
-      float v = 0.f;
-      for (int k = 0; k < nw; k++) v += s_sum[k * TOK * kGemvRows + i];
-      const int tok = i / kGemvRows, row = row0 + i % kGemvRows;
-      if (row < A.rows) put_y(A, (int64_t)tok * A.rows + row, v);
-    }
-    return;
-  }
-  float* hbuf = s_sum + (size_t)nw * M * TOK * kGemvRows;  // [tokens][16]
-  const uint32_t rank = cluster_rank();
-  cluster_wait();
-  for (int i = threadIdx.x; i < TOK * kGemvRows; i += blockDim.x) {  // whole half-warps
-    float gv = 0.f, uv = 0.f;
-    for (int k = 0; k < nw; k++) {
-      gv += s_sum[(k * M) * TOK * kGemvRows + i];
-      uv += s_sum[(k * M + M - 1) * TOK * kGemvRows + i];
-    }
-    const float h = silu_f32(gv) * uv;
-    hbuf[i] = h;
-    float m = row0 + i % kGemvRows < A.rows ? magnitude(h) : 0.f;
-#pragma unroll
-    for (int d = 8; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    if (i % kGemvRows < kGuCluster) st_peer(peer_smem(&s_amax[rank][i / kGemvRows], i % kGemvRows), m);
-  }
-  cluster_arrive();
-  cluster_wait();
-  if (row0 >= A.rows) return;
-  for (int i = threadIdx.x; i < A.T * 4; i += blockDim.x) {  // four rows of one token each
-    const int tok = i / 4, r = 4 * (i % 4);
-    float most = 0.f;
-#pragma unroll
-    for (int k = 0; k < kGuCluster; k++) most = fmaxf(most, s_amax[k][tok]);
-    const bool fine = most <= 3.402823466e38f;
-    most = fmaxf(most, kAmaxMin);
-    const float inv = fine ? kE4m3Max / most : 0.f;
-    const float4 h = *reinterpret_cast<const float4*>(hbuf + tok * kGemvRows + r);
-    const uint32_t o = fine ? e4m3x4(h.x * inv, h.y * inv, h.z * inv, h.w * inv) : 0u;
-    *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(A.y) + (int64_t)tok * A.rows + row0 + r) = o;
-    if (rank == 0 && r == 0)
-      A.hs[(int64_t)tok * ((A.rows + kFp8Block - 1) / kFp8Block) + row0 / kFp8Block] =
-          fine ? most / kE4m3Max : __int_as_float(0x7fffffff);
-  }
 }
 
 // ----------------------------------------------------------- many tokens
@@ -422,6 +235,22 @@ __device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32]) {
                : "memory");
 }
 
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait_ld16(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+
 // Two float32 fused multiply-adds in one instruction: acc += (lo, hi) * (s, s).
 __device__ __forceinline__ void fma2(uint64_t& acc, uint32_t lo, uint32_t hi, uint64_t s) {
   asm("{\n\t.reg .b64 v;\n\tmov.b64 v, {%1, %2};\n\tfma.rn.f32x2 %0, v, %3, %0;\n\t}"
@@ -468,6 +297,49 @@ __device__ __forceinline__ void put_y4(const Fp8Args& A, int64_t t, int n, float
       v.w += __uint_as_float(a.y & 0xffff0000u);
     }
     *reinterpret_cast<uint2*>(static_cast<uint16_t*>(A.y) + i) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+  }
+}
+
+// One warp ends one token's row of V * 128 columns: the sum over the cluster's
+// CTAs of the accumulators at `src` in each one's shared memory, in rank order,
+// and what becomes of it. Gate_up: 128 gate columns, then their up columns.
+template <int V, bool GU>
+__device__ __forceinline__ void finish_row(const Fp8Args& A, const float* src, int split, int64_t t, int n0, int lane) {
+  float4 v[V];
+#pragma unroll
+  for (int h = 0; h < V; h++) {
+    v[h] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (split == 1) {
+      v[h] = *reinterpret_cast<const float4*>(src + 128 * h + 4 * lane);
+    } else {
+      for (int k = 0; k < split; k++) {
+        const float4 o = ld_peer4(peer_smem(src + 128 * h + 4 * lane, k));
+        v[h].x += o.x;
+        v[h].y += o.y;
+        v[h].z += o.z;
+        v[h].w += o.w;
+      }
+    }
+  }
+  const int n = n0 + 4 * lane;
+  if (GU) {
+    const float4 gv = v[0], uv = v[V - 1];
+    const float h0 = silu_f32(gv.x) * uv.x, h1 = silu_f32(gv.y) * uv.y, h2 = silu_f32(gv.z) * uv.z,
+                h3 = silu_f32(gv.w) * uv.w;
+    float most = n < A.rows ? fmaxf(fmaxf(magnitude(h0), magnitude(h1)), fmaxf(magnitude(h2), magnitude(h3))) : 0.f;
+#pragma unroll
+    for (int d = 16; d; d >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
+    const bool fine = most <= 3.402823466e38f;
+    most = fmaxf(most, kAmaxMin);
+    const float inv = fine ? kE4m3Max / most : 0.f;
+    const uint32_t o = fine ? e4m3x4(h0 * inv, h1 * inv, h2 * inv, h3 * inv) : 0u;
+    if (n < A.rows) *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(A.y) + t * A.rows + n) = o;
+    if (lane == 0)
+      A.hs[t * ((A.rows + kFp8Block - 1) / kFp8Block) + n0 / kFp8Block] =
+          fine ? most / kE4m3Max : __int_as_float(0x7fffffff);
+  } else {
+#pragma unroll
+    for (int h = 0; h < V; h++) put_y4(A, t, n + 128 * h, v[h]);
   }
 }
 
@@ -720,45 +592,194 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   // One warp per row, rows dealt to the cluster's CTAs and their warps in turn.
   const int t0 = (first % tiles_m) * kBM, n0 = (first / tiles_m) * NB;
   const int nrow = min(kBM, A.T - t0);
-  for (int r = rank + split * warp; r < nrow; r += split * kEpiWarps) {
-    float4 v[BN / 128];
-#pragma unroll
-    for (int h = 0; h < BN / 128; h++) {
-      const float* src = reinterpret_cast<const float*>(smem) + (size_t)r * kPitch(BN) + 128 * h + 4 * lane;
-      v[h] = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int k = 0; k < split; k++) {
-        const float4 o = ld_peer4(peer_smem(src, k));
-        v[h].x += o.x;
-        v[h].y += o.y;
-        v[h].z += o.z;
-        v[h].w += o.w;
-      }
-    }
-    const int64_t t = t0 + r;
-    const int n = n0 + 4 * lane;
-    if (GU) {
-      const float4 gv = v[0], uv = v[BN / 128 - 1];
-      const float h0 = silu_f32(gv.x) * uv.x, h1 = silu_f32(gv.y) * uv.y, h2 = silu_f32(gv.z) * uv.z,
-                  h3 = silu_f32(gv.w) * uv.w;
-      float most =
-          n < A.rows ? fmaxf(fmaxf(magnitude(h0), magnitude(h1)), fmaxf(magnitude(h2), magnitude(h3))) : 0.f;
-#pragma unroll
-      for (int d = 16; d; d >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
-      const bool fine = most <= 3.402823466e38f;
-      most = fmaxf(most, kAmaxMin);
-      const float inv = fine ? kE4m3Max / most : 0.f;
-      const uint32_t o = fine ? e4m3x4(h0 * inv, h1 * inv, h2 * inv, h3 * inv) : 0u;
-      if (n < A.rows) *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(A.y) + t * A.rows + n) = o;
-      if (lane == 0)
-        A.hs[t * ((A.rows + kFp8Block - 1) / kFp8Block) + n0 / kFp8Block] =
-            fine ? most / kE4m3Max : __int_as_float(0x7fffffff);
-    } else {
-#pragma unroll
-      for (int h = 0; h < BN / 128; h++) put_y4(A, t, n + 128 * h, v[h]);
-    }
-  }
+  for (int r = rank + split * warp; r < nrow; r += split * kEpiWarps)
+    finish_row<BN / 128, GU>(A, reinterpret_cast<const float*>(smem) + (size_t)r * kPitch(BN), split, t0 + r, n0, lane);
   cluster_arrive();  // the peers have read this CTA's accumulators
   cluster_wait();
+}
+
+// ---------------------------------------------------------------- few tokens
+//
+// The same with the operands' places changed: M = 128 weight rows (gate_up: two
+// MMAs, of 128 gate and of 128 up rows), N = the tokens, padded to TN. A step
+// then costs the tensor cores what its weights' bytes cost to read, where 128
+// token rows would be mostly padding. Thread = weight row; the token scales,
+// times the block's, come from a table that each warp writes for each step.
+constexpr int kSkinnyThreads = 6 * 32;
+constexpr int kSkinnyMaxT = 32;
+constexpr int kSkStage(bool gu, int TN) { return ((gu ? 256 : 128) + TN) * kFp8Block; }
+constexpr int kSkStages(bool gu) { return gu ? 3 : 5; }
+constexpr int kSkBufs = 4;  // accumulators in tensor memory: at most 256 columns for each of two CTAs
+constexpr int kSkRing(bool gu, int TN) { return kSkStages(gu) * kSkStage(gu, TN); }
+constexpr size_t kSkSmem(bool gu, int TN) { return kSkRing(gu, TN) + 4 * 2 * kSkinnyMaxT * 4 + 256 + 1024; }
+static_assert(kSkRing(true, 32) >= 32 * 256 * 4 && kSkRing(false, 32) >= 32 * 128 * 4, "accumulators");
+static_assert(kSkSmem(true, 32) <= 113 * 1024 && kSkSmem(false, 32) <= 113 * 1024, "two CTAs on an SM");
+
+template <bool GU, int TN>
+__global__ void __launch_bounds__(kSkinnyThreads, 2)
+    k_fp8_skinny(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap m0,
+                 const __grid_constant__ CUtensorMap m1, const __grid_constant__ Fp8Args A, int split) {
+  constexpr int M = GU ? 2 : 1, ST = kSkStages(GU), SB = kSkStage(GU, TN), NBUF = kSkBufs;
+  constexpr int COLS = NBUF * TN * M, LD = TN < 32 ? 16 : 32;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  float* table = reinterpret_cast<float*>(smem + kSkRing(GU, TN));  // [4 warps][2][32]
+  uint64_t* full = reinterpret_cast<uint64_t*>(table + 4 * 2 * kSkinnyMaxT);
+  uint64_t* empty = full + ST;
+  uint64_t* tfull = empty + ST;
+  uint64_t* tfree = tfull + NBUF;
+  uint64_t* drain = tfree + NBUF;
+  uint32_t* holder = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile uint32_t* abort_flag = holder + 1;
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+  const int rank = split > 1 ? (int)cluster_rank() : 0;
+  const int n0 = (int)(blockIdx.x / split) * 128;
+  const int kb_lo = (int)((int64_t)A.nkb * rank / split), kb_hi = (int)((int64_t)A.nkb * (rank + 1) / split);
+  const int steps = kb_hi - kb_lo;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < ST; i++) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < NBUF; i++) {
+      mbar_init(&tfull[i], 1);
+      mbar_init(&tfree[i], 4);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 4 && lane == 0) {
+    prefetch_tensormap(&mx);
+    prefetch_tensormap(&m0);
+    prefetch_tensormap(&m1);
+  }
+  if (warp == 5) tmem_alloc(holder, COLS);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *holder;
+  griddep_wait();
+  griddep_launch();
+
+  if (warp == 4) {
+    const bool leader = elect_one();
+    int i = 0;
+    for (; i < steps; i++) {
+      const int s = i % ST, k = (kb_lo + i) * kFp8Block;
+      if (!gemm_wait(&empty[s], ((i / ST) & 1) ^ 1, abort_flag)) break;
+      if (leader) {
+        uint8_t* a = smem + s * SB;
+        mbar_arrive_expect_tx(&full[s], SB);
+        tma_load_2d(a, &m0, k, n0, &full[s]);
+        if (GU) tma_load_2d(a + 128 * kFp8Block, &m1, k, n0, &full[s]);
+        tma_load_2d(a + M * 128 * kFp8Block, &mx, k, 0, &full[s]);
+      }
+      __syncwarp();
+    }
+    if (i < steps)  // a wait expired: let the copies in flight land
+      for (int j = i < ST ? 0 : i - ST; j < i; j++) mbar_wait_ns(&full[j % ST], (j / ST) & 1, kDrainWaitNs);
+  } else if (warp == 5) {
+    const bool leader = elect_one();
+    const uint64_t d0 = sdesc_kmajor_sw128(smem_u32(smem));
+    int i = 0;
+    for (; i < steps; i++) {
+      const int s = i % ST, b = i % NBUF;
+      if (!gemm_wait(&full[s], (i / ST) & 1, abort_flag) || !gemm_wait(&tfree[b], ((i / NBUF) & 1) ^ 1, abort_flag)) break;
+      tc_fence_after();
+      if (leader) {
+        const uint64_t dw = d0 + (uint32_t)(s * (SB / 16)), dx = dw + M * 128 * kFp8Block / 16;
+#pragma unroll
+        for (int m = 0; m < M; m++)
+#pragma unroll
+          for (int j = 0; j < 4; j++)
+            mma_ss_e4m3(tmem + (b * M + m) * TN, dw + (uint32_t)(m * 128 * kFp8Block / 16) + 2u * j, dx + 2u * j,
+                        idesc_e4m3_m128(TN), j != 0);
+        tc_commit(&tfull[b]);
+        tc_commit(&empty[s]);
+      }
+      __syncwarp();
+    }
+    if (i < steps) {  // a wait expired: let the products in flight end before their tensor memory is given back
+      if (leader) tc_commit(drain);
+      mbar_wait_ns(drain, 0, kDrainWaitNs);
+    }
+  } else {
+    const int wb = min(n0, A.rows - 1) / kFp8Block;
+    const float* ws = A.w0.s + (int64_t)wb * A.nkb + kb_lo;
+    const float* us = A.w1.s + (int64_t)wb * A.nkb + kb_lo;
+    const float* xs = A.xs + (int64_t)min(lane, A.T - 1) * A.nkb + kb_lo;
+    float* tab = table + warp * 2 * kSkinnyMaxT;  // [gate, up][token]
+    const uint32_t lanes = tmem + ((uint32_t)(32 * warp) << 16);
+    uint64_t acc[M][TN / 2];
+#pragma unroll
+    for (int m = 0; m < M; m++)
+#pragma unroll
+      for (int c = 0; c < TN / 2; c++) acc[m][c] = 0;
+    float xn = xs[0], wn = ws[0], un = GU ? us[0] : 0.f;
+    bool ok = true;
+    for (int i = 0; i < steps; i++) {
+      const int b = i % NBUF;
+      __syncwarp();
+      tab[lane] = xn * wn;
+      if (GU) tab[kSkinnyMaxT + lane] = xn * un;
+      if (i + 1 < steps) {
+        xn = xs[i + 1];
+        wn = ws[i + 1];
+        if (GU) un = us[i + 1];
+      }
+      __syncwarp();
+      if (!(ok = gemm_wait(&tfull[b], (i / NBUF) & 1, abort_flag))) break;
+      tc_fence_after();
+#pragma unroll
+      for (int m = 0; m < M; m++)
+#pragma unroll
+        for (int c0 = 0; c0 < TN; c0 += LD) {
+          uint32_t r[LD];
+          if constexpr (LD == 16) {
+            tmem_ld16(lanes + (b * M + m) * TN + c0, r);
+            tmem_wait_ld16(r);
+          } else {
+            tmem_ld32(lanes + (b * M + m) * TN + c0, r);
+            tmem_wait_ld(r);
+          }
+#pragma unroll
+          for (int c = 0; c < LD; c += 4) {
+            const ulonglong2 sc = *reinterpret_cast<const ulonglong2*>(tab + m * kSkinnyMaxT + c0 + c);
+            fma2(acc[m][(c0 + c) / 2], r[c], r[c + 1], sc.x);
+            fma2(acc[m][(c0 + c) / 2 + 1], r[c + 2], r[c + 3], sc.y);
+          }
+        }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&tfree[b]);
+    }
+    if (ok) {
+      // All MMAs have read their operands: the ring takes the accumulators, [token][128 or 256 rows].
+      float* dst = reinterpret_cast<float*>(smem) + 32 * warp + lane;
+#pragma unroll
+      for (int m = 0; m < M; m++)
+#pragma unroll
+        for (int c = 0; c < TN; c++)
+          if (c < A.T) dst[c * (M * 128) + m * 128] = (c & 1) ? hi_of(acc[m][c / 2]) : lo_of(acc[m][c / 2]);
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 5) tmem_dealloc(tmem, COLS);
+  if (split > 1) {
+    cluster_arrive();
+    cluster_wait();
+  }
+  for (int t = rank + split * warp; t < A.T; t += split * (kSkinnyThreads / 32))
+    finish_row<M, GU>(A, reinterpret_cast<const float*>(smem) + (size_t)t * (M * 128), split, t, n0, lane);
+  if (split > 1) {  // the peers have read this CTA's accumulators
+    cluster_arrive();
+    cluster_wait();
+  }
 }
 
 cudaLaunchAttribute pdl() {
@@ -788,34 +809,13 @@ int allow_smem() {
   return 0;
 }
 
-size_t gemv_smem_bytes(int T, int nkb, int nw, int nt, bool gu) {
-  return gemv_x_bytes(T, nkb, gu ? 2 : 1) + (size_t)(nw * (gu ? 2 : 1) + (gu ? 1 : 0)) * 8 * nt * kGemvRows * 4;
-}
-
-template <int NT, bool GU, int U>
-int launch_gemv_nt(const Fp8Args& a, cudaStream_t st) {
-  const int nw = std::min(kGemvWarps, (a.nkb + U - 1) / U);
-  const int tiles = (a.rows + kGemvRows - 1) / kGemvRows;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(GU ? (tiles + kGuCluster - 1) / kGuCluster * kGuCluster : tiles));
-  cfg.blockDim = dim3((unsigned)nw * 32);
-  cfg.dynamicSmemBytes = gemv_smem_bytes(a.T, a.nkb, nw, NT, GU);
-  auto kern = k_fp8_gemv<NT, GU, U>;
-  if (cfg.dynamicSmemBytes > 47 * 1024 && allow_smem<k_fp8_gemv<NT, GU, U>, kGemvSmemMax>()) return -4;
-  cfg.stream = st;
-  cudaLaunchAttribute at[2] = {pdl(), cluster_of(kGuCluster)};
-  cfg.attrs = at;
-  cfg.numAttrs = GU ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kern, a) == cudaSuccess ? 0 : -4;
-}
-
-// Map of a row-major e4m3 matrix, boxes of 128 rows x 128 columns; columns and rows past the end read as zero.
-int make_e4m3_map(CUtensorMap* map, const uint8_t* base, int rows, int cols) {
+// Map of a row-major e4m3 matrix, boxes of box_rows x 128 columns; columns and rows past the end read as zero.
+int make_e4m3_map(CUtensorMap* map, const uint8_t* base, int rows, int cols, int box_rows) {
   EncodeTiledFn enc = encode_tiled_fn();
   if (!enc) return -4;
   const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
   const cuuint64_t strides[1] = {(cuuint64_t)cols};
-  const cuuint32_t box[2] = {(cuuint32_t)kFp8Block, 128};
+  const cuuint32_t box[2] = {(cuuint32_t)kFp8Block, (cuuint32_t)box_rows};
   const cuuint32_t estr[2] = {1, 1};
   const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(base), dims, strides, box, estr,
                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -823,16 +823,49 @@ int make_e4m3_map(CUtensorMap* map, const uint8_t* base, int rows, int cols) {
   return r == CUDA_SUCCESS ? 0 : -4;
 }
 
+// CTAs that a tile's blocks are split over: the least time by the steps in a
+// row, times the waves that the clusters need (a cluster lives inside one GPC,
+// so 8 CTAs of one per SM fit 15 times, not 18, into 148 SMs).
+constexpr int kMaxSplit = 8;
+constexpr int kTileSteps = 6;   // start, drain and stores of a tile, in steps
+constexpr int kSplitSteps = 6;  // the exchange between the CTAs of a cluster
+
+template <auto KERN, size_t SMEM, int THREADS>
+int pick_split(int64_t tiles, int nkb, int at_once) {
+  static std::atomic<int> fit[64][kMaxSplit + 1];  // clusters that run at once; 0: not asked yet
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return -4;
+  int best = 1;
+  int64_t least = (tiles + at_once - 1) / at_once * (nkb + kTileSteps);
+  for (int split = 2; split <= kMaxSplit && split <= nkb && tiles * split <= at_once; split++) {
+    int n = dev < 64 ? fit[dev][split].load(std::memory_order_relaxed) : 0;
+    if (n == 0) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3((unsigned)split);
+      cfg.blockDim = dim3(THREADS);
+      cfg.dynamicSmemBytes = SMEM;
+      cudaLaunchAttribute at[1] = {cluster_of(split)};
+      cfg.attrs = at;
+      cfg.numAttrs = 1;
+      if (cudaOccupancyMaxActiveClusters(&n, KERN, &cfg) != cudaSuccess) return -4;
+      if (n < 1) n = -1;
+      if (dev < 64) fit[dev][split].store(n, std::memory_order_relaxed);
+    }
+    if (n < 1) continue;
+    const int64_t cost = (tiles + n - 1) / n * ((nkb + split - 1) / split + kTileSteps + kSplitSteps);
+    if (cost < least) {
+      least = cost;
+      best = split;
+    }
+  }
+  return best;
+}
+
 template <int BN, bool GU>
 int launch_gemm(const Fp8Args& a, int num_sms, cudaStream_t st) {
   const int tiles_m = (a.T + kBM - 1) / kBM, nb = GU ? 128 : BN, tiles_n = (a.rows + nb - 1) / nb;
   const int64_t tiles = (int64_t)tiles_m * tiles_n;
   if (tiles > 0x0fffffff) return -3;
-  int split = 1;
-  while (split < 8 && tiles * split * 2 <= num_sms && split * 2 <= a.nkb) split *= 2;
-  CUtensorMap mx, m0, m1;
-  if (make_e4m3_map(&mx, a.xq, a.T, a.cols) || make_e4m3_map(&m0, a.w0.q, a.rows, a.cols)) return -4;
-  if (GU ? make_e4m3_map(&m1, a.w1.q, a.rows, a.cols) != 0 : (m1 = m0, false)) return -4;
   auto kern = k_fp8_gemm<BN, GU>;
   static std::atomic<bool> checked{false};
   if (!checked.load(std::memory_order_relaxed)) {
@@ -843,6 +876,11 @@ int launch_gemm(const Fp8Args& a, int num_sms, cudaStream_t st) {
     checked.store(true);
   }
   if (allow_smem<k_fp8_gemm<BN, GU>, kGemmSmem(BN)>()) return -4;
+  const int split = pick_split<k_fp8_gemm<BN, GU>, kGemmSmem(BN), kGemmThreads>(tiles, a.nkb, num_sms);
+  if (split < 1) return split;
+  CUtensorMap mx, m0, m1;
+  if (make_e4m3_map(&mx, a.xq, a.T, a.cols, kBM) || make_e4m3_map(&m0, a.w0.q, a.rows, a.cols, 128)) return -4;
+  if (GU ? make_e4m3_map(&m1, a.w1.q, a.rows, a.cols, 128) != 0 : (m1 = m0, false)) return -4;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(split > 1 ? tiles * split : std::min<int64_t>(tiles, num_sms)));
   cfg.blockDim = dim3(kGemmThreads);
@@ -852,6 +890,27 @@ int launch_gemm(const Fp8Args& a, int num_sms, cudaStream_t st) {
   cfg.attrs = at;
   cfg.numAttrs = split > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, mx, m0, m1, a, tiles_m, (int)tiles, split) == cudaSuccess ? 0 : -4;
+}
+
+template <bool GU, int TN>
+int launch_skinny(const Fp8Args& a, int num_sms, cudaStream_t st) {
+  constexpr size_t smem = kSkSmem(GU, TN);
+  const int tiles = (a.rows + 127) / 128;
+  if (allow_smem<k_fp8_skinny<GU, TN>, smem>()) return -4;
+  const int split = pick_split<k_fp8_skinny<GU, TN>, smem, kSkinnyThreads>(tiles, a.nkb, 2 * num_sms);
+  if (split < 1) return split;
+  CUtensorMap mx, m0, m1;
+  if (make_e4m3_map(&mx, a.xq, a.T, a.cols, TN) || make_e4m3_map(&m0, a.w0.q, a.rows, a.cols, 128)) return -4;
+  if (GU ? make_e4m3_map(&m1, a.w1.q, a.rows, a.cols, 128) != 0 : (m1 = m0, false)) return -4;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(tiles * split));
+  cfg.blockDim = dim3(kSkinnyThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[2] = {pdl(), cluster_of(split)};
+  cfg.attrs = at;
+  cfg.numAttrs = split > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, k_fp8_skinny<GU, TN>, mx, m0, m1, a, split) == cudaSuccess ? 0 : -4;
 }
 
 }  // namespace
@@ -874,9 +933,9 @@ int launch_fp8_quantize(const uint16_t* x, int64_t stride, int T, int cols, uint
 }
 
 int launch_fp8_product(const Fp8Args& a, bool gate_up, cudaStream_t st, int num_sms) {
-  if (a.T <= kGemvMaxT && gemv_smem_bytes(a.T, a.nkb, kGemvWarps, a.T <= 8 ? 1 : 2, gate_up) <= kGemvSmemMax) {
-    if (gate_up) return a.T <= 8 ? launch_gemv_nt<1, true, 2>(a, st) : launch_gemv_nt<2, true, 2>(a, st);
-    return a.T <= 8 ? launch_gemv_nt<1, false, 4>(a, st) : launch_gemv_nt<2, false, 4>(a, st);
+  if (a.T <= kSkinnyMaxT) {
+    if (gate_up) return a.T <= 16 ? launch_skinny<true, 16>(a, num_sms, st) : launch_skinny<true, 32>(a, num_sms, st);
+    return a.T <= 16 ? launch_skinny<false, 16>(a, num_sms, st) : launch_skinny<false, 32>(a, num_sms, st);
   }
   if (gate_up) return launch_gemm<256, true>(a, num_sms, st);
   const int64_t tiles = (int64_t)((a.T + kBM - 1) / kBM) * ((a.rows + 255) / 256);
