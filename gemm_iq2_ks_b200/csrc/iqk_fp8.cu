@@ -163,46 +163,83 @@ __device__ __forceinline__ float magnitude(float h) {  // infinity for what is n
 // tiles the CTAs of a cluster split the blocks of one tile and add their
 // accumulators over distributed shared memory, in rank order.
 constexpr int kBM = 128;
-constexpr int kEpiWarps = 16, kTmaWarp = 16, kMmaWarp = 17;
-constexpr int kGemmThreads = 20 * 32;  // the last warpgroup: copies, MMAs and two idle warps
+constexpr int kEpiWarps = 16, kTmaWarp = 16, kMmaWarp = 17, kScaleWarp = 18;  // and 19
+constexpr int kGemmThreads = 20 * 32;
 // Registers: 640 threads are launched with 96 each; the accumulating warps take
 // 112, the last warpgroup keeps 32 (4 x 112 + 32 = 5 x 96).
 constexpr int kEpiRegs = 112, kLastRegs = 32;
-constexpr int kGemmStageBytes(int BN) { return (kBM + BN) * kFp8Block; }
-constexpr int kGemmStages(int BN) { return BN == 256 ? 4 : 6; }
-constexpr int kGemmRing(int BN) { return kGemmStages(BN) * kGemmStageBytes(BN); }
+constexpr int kGemmStageBytes(int BN, bool pair) { return (kBM + (pair ? BN / 2 : BN)) * kFp8Block; }
+constexpr int kGemmRing(int BN, bool pair) { return (BN == 256 && !pair ? 4 : 5) * kGemmStageBytes(BN, pair); }
 constexpr int kPitch(int BN) { return BN + 4; }  // floats between rows of the shared accumulators
 constexpr int kStageOut = 2048;                  // bytes of one warp's store staging: 32 rows x 16 floats
-constexpr size_t kGemmSmem(int BN) { return kGemmRing(BN) + kEpiWarps * kStageOut + 256 + 1024; }
-static_assert(kBM * kPitch(256) * 4 <= kGemmRing(256) && kBM * kPitch(128) * 4 <= kGemmRing(128), "accumulators");
+constexpr int kStaging(bool gu) { return gu ? 4 * kBM * 4 : kEpiWarps * kStageOut; }
+// With the scales of a step beside each accumulator: [2 weight blocks][128 rows]
+// products of token and block scale, written by two warps of their own.
+constexpr size_t kGemmSmem(int BN, bool gu, bool pair) {
+  return kGemmRing(BN, pair) + kStaging(gu) + 512 / BN * 2 * kBM * 4 + 256 + 1024;
+}
+static_assert(kBM * kPitch(256) * 4 <= kGemmRing(256, false) && kBM * kPitch(128) * 4 <= kGemmRing(128, false),
+              "accumulators");
 
-// Bounded wait: gives up after kDefaultWaitNs of the global timer, or soon
-// after another warp of the CTA did.
+// Bounded wait: gives up after a million tries (each of which the hardware
+// suspends for a while: seconds in all), or soon after another warp of the CTA did.
 __device__ __forceinline__ bool gemm_wait(uint64_t* bar, uint32_t par, volatile uint32_t* abort_flag) {
-  if (mbar_try_wait(bar, par)) return true;
-  uint64_t t0 = 0;
-  for (uint32_t i = 1;; i++) {
+  for (uint32_t i = 0; i < (1u << 20); i++) {
     if (mbar_try_wait(bar, par)) return true;
-    if (i % 256 == 0) {
-      if (*abort_flag) return false;
-      const uint64_t now = globaltimer_ns();
-      if (t0 == 0) t0 = now;
-      if (now - t0 >= kDefaultWaitNs) break;
-    }
+    if (i % 256 == 255 && *abort_flag) return false;
   }
   *abort_flag = 1;
   atomicOr(&g_fp8_status, 2);
   return false;
 }
 
+template <bool PAIR = false>
 __device__ __forceinline__ void mma_ss_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                             uint32_t accumulate) {
+  if (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Two CTAs of a cluster as one (cta_group::2): tensor memory, the copy whose
+// bytes count on the first CTA's barrier, the commit that arrives in both, the
+// arrival in the first.
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t* holder_smem, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(holder_smem)),
+               "r"(ncols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t base, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(ncols) : "memory");
+}
+__device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* map, int32_t x, int32_t y, uint32_t bar) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+      "[%4];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
       : "memory");
+}
+__device__ __forceinline__ void tc_commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_peer(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // One lane of a converged warp: the copies and MMAs are issued under it, from
@@ -266,9 +303,9 @@ __device__ __forceinline__ float lo_of(uint64_t v) { return __uint_as_float((uin
 __device__ __forceinline__ float hi_of(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
 
 // Instruction descriptor, kind::f8f6f4: e4m3 A and B (format code 0), float32
-// accumulator, both K-major, M = 128, N = n.
-__host__ __device__ constexpr uint32_t idesc_e4m3_m128(uint32_t n) {
-  return (1u << 4) | ((n >> 3) << 17) | ((128u >> 4) << 24);
+// accumulator, both K-major.
+__host__ __device__ constexpr uint32_t idesc_e4m3(uint32_t m, uint32_t n) {
+  return (1u << 4) | ((n >> 3) << 17) | ((m >> 4) << 24);
 }
 
 // Four neighbouring outputs of one row; A.vec: rows and pointers allow vector access.
@@ -343,27 +380,31 @@ __device__ __forceinline__ void finish_row(const Fp8Args& A, const float* src, i
   }
 }
 
-template <int BN, bool GU>
+template <int BN, bool GU, bool PAIR>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     k_fp8_gemm(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap m0,
                const __grid_constant__ CUtensorMap m1, const __grid_constant__ Fp8Args A, int tiles_m, int tiles,
                int split) {
-  constexpr int ST = kGemmStages(BN), SB = kGemmStageBytes(BN), NC = BN / 4;
+  constexpr int SB = kGemmStageBytes(BN, PAIR), ST = kGemmRing(BN, PAIR) / SB, NC = BN / 4;
   constexpr int NBUF = 512 / BN;  // accumulators in tensor memory
   constexpr int NB = GU ? 128 : BN;  // output columns of a tile
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-  uint8_t* staging = smem + kGemmRing(BN);
-  uint64_t* full = reinterpret_cast<uint64_t*>(staging + kEpiWarps * kStageOut);
+  uint8_t* staging = smem + kGemmRing(BN, PAIR);
+  float* scales = reinterpret_cast<float*>(staging + kStaging(GU));
+  uint64_t* full = reinterpret_cast<uint64_t*>(scales + NBUF * 2 * kBM);
   uint64_t* empty = full + ST;
   uint64_t* tfull = empty + ST;
-  uint64_t* tfree = tfull + 4;
-  uint64_t* drain = tfree + 4;
+  uint64_t* tfree = tfull + NBUF;
+  uint64_t* sfree = tfree + NBUF;
+  uint64_t* drain = sfree + NBUF;
   uint32_t* holder = reinterpret_cast<uint32_t*>(drain + 1);
   volatile uint32_t* abort_flag = holder + 1;
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
-  const int rank = split > 1 ? (int)cluster_rank() : 0;
-  const int first = blockIdx.x / split, step = gridDim.x / split;
+  // PAIR: `split` is 1 and the cluster's two CTAs take the halves of a tile's 256 tokens.
+  const int rank = split > 1 ? (int)cluster_rank() : 0, half = PAIR ? (int)cluster_rank() : 0;
+  const int group = PAIR ? 2 : split;
+  const int first = blockIdx.x / group, step = gridDim.x / group;
   const int kb_lo = (int)((int64_t)A.nkb * rank / split), kb_hi = (int)((int64_t)A.nkb * (rank + 1) / split);
   const int steps = kb_hi - kb_lo;
 
@@ -373,8 +414,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < NBUF; i++) {
-      mbar_init(&tfull[i], 1);
-      mbar_init(&tfree[i], kEpiWarps);
+      mbar_init(&tfull[i], 3);  // the commit and the two scale warps
+      mbar_init(&tfree[i], PAIR ? 2 * kEpiWarps : kEpiWarps);
+      mbar_init(&sfree[i], kEpiWarps);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -385,9 +427,18 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     prefetch_tensormap(&m0);
     prefetch_tensormap(&m1);
   }
-  if (warp == kMmaWarp) tmem_alloc(holder, 512);
+  if (warp == kMmaWarp) {
+    if (PAIR)
+      tmem_alloc_pair(holder, 512);
+    else
+      tmem_alloc(holder, 512);
+  }
   tc_fence_before();
   __syncthreads();
+  if (PAIR) {  // both CTAs' barriers and tensor memory are ready
+    cluster_arrive();
+    cluster_wait();
+  }
   tc_fence_after();
   const uint32_t tmem = *holder;
   griddep_wait();
@@ -400,25 +451,35 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       int it = 0;
       bool ok = true;
       for (int tile = first; tile < tiles && ok; tile += step) {
-        const int t0 = (tile % tiles_m) * kBM, n0 = (tile / tiles_m) * NB;
+        const int t0 = (tile % tiles_m * (PAIR ? 2 : 1) + half) * kBM, n0 = (tile / tiles_m) * NB;
         for (int i = 0; i < steps; i++, it++) {
           const int s = it % ST, k = (kb_lo + i) * kFp8Block;
           if (!(ok = gemm_wait(&empty[s], ((it / ST) & 1) ^ 1, abort_flag))) break;
           if (leader) {
             uint8_t* a = smem + s * SB;
             uint8_t* w = a + kBM * kFp8Block;
-            mbar_arrive_expect_tx(&full[s], SB);
-            tma_load_2d(a, &mx, k, t0, &full[s]);
-            tma_load_2d(w, &m0, k, n0, &full[s]);
-            if (BN == 256) tma_load_2d(w + 128 * kFp8Block, &m1, k, GU ? n0 : n0 + 128, &full[s]);
+            if (PAIR) {  // each CTA: its tokens and half of the weight rows (gate_up: gate or up)
+              if (half == 0) mbar_arrive_expect_tx(&full[s], 2 * SB);
+              const uint32_t bar = peer_smem(&full[s], 0);
+              tma_load_2d_pair(a, &mx, k, t0, bar);
+              tma_load_2d_pair(w, GU && half ? &m1 : &m0, k, GU ? n0 : n0 + 128 * half, bar);
+            } else {
+              mbar_arrive_expect_tx(&full[s], SB);
+              tma_load_2d(a, &mx, k, t0, &full[s]);
+              tma_load_2d(w, &m0, k, n0, &full[s]);
+              if (BN == 256) tma_load_2d(w + 128 * kFp8Block, &m1, k, GU ? n0 : n0 + 128, &full[s]);
+            }
           }
           __syncwarp();
         }
       }
-      if (!ok)  // a wait expired: let the copies in flight land
+      if (!ok && half == 0)  // a wait expired: let the copies in flight land
         for (int j = it < ST ? 0 : it - ST; j < it; j++) mbar_wait_ns(&full[j % ST], (j / ST) & 1, kDrainWaitNs);
+      if (!ok && half)  // these count on the other CTA's barriers: a time that copies do not take
+        for (const uint64_t t = globaltimer_ns(); globaltimer_ns() - t < 10000000ull;) {
+        }
     }
-    if (warp == kMmaWarp) {
+    if (warp == kMmaWarp && half == 0) {
       const bool leader = elect_one();
       // descriptors differ in the address field (bytes / 16) only
       const uint64_t d0 = sdesc_kmajor_sw128(smem_u32(smem));
@@ -434,22 +495,73 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           if (leader) {
             const uint64_t da = d0 + (uint32_t)(s * (SB / 16)), dw = da + kBM * kFp8Block / 16;
 #pragma unroll
-            for (int j = 0; j < 4; j++) mma_ss_e4m3(tmem + b * BN, da + 2u * j, dw + 2u * j, idesc_e4m3_m128(BN), j != 0);
-            tc_commit(&tfull[b]);
-            tc_commit(&empty[s]);
+            for (int j = 0; j < 4; j++)
+              mma_ss_e4m3<PAIR>(tmem + b * BN, da + 2u * j, dw + 2u * j, idesc_e4m3(PAIR ? 256 : 128, BN), j != 0);
+            if (PAIR) {
+              tc_commit_pair(&tfull[b]);
+              tc_commit_pair(&empty[s]);
+            } else {
+              tc_commit(&tfull[b]);
+              tc_commit(&empty[s]);
+            }
           }
           __syncwarp();
         }
       }
       if (!ok) {  // a wait expired: let the products in flight end before their tensor memory is given back
-        if (leader) tc_commit(drain);
+        if (leader) {
+          if (PAIR)
+            tc_commit_pair(drain);
+          else
+            tc_commit(drain);
+        }
         mbar_wait_ns(drain, 0, kDrainWaitNs);
+      }
+    }
+    if (warp >= kScaleWarp) {
+      // rows 64 w + lane and 32 on, one step's scales fetched ahead
+      const int r = 64 * (warp - kScaleWarp) + lane;
+      int it = 0;
+      bool ok = true;
+      for (int tile = first; tile < tiles && ok; tile += step) {
+        const int t0 = (tile % tiles_m * (PAIR ? 2 : 1) + half) * kBM, n0 = (tile / tiles_m) * NB;
+        const int last = (A.rows - 1) / kFp8Block;  // blocks past it: any, their columns are not stored
+        uint32_t x0 = (uint32_t)min(t0 + r, A.T - 1) * A.nkb + kb_lo, x1 = (uint32_t)min(t0 + r + 32, A.T - 1) * A.nkb + kb_lo;
+        const uint32_t w0 = (uint32_t)min(n0 / kFp8Block, last) * A.nkb + kb_lo;
+        const uint32_t w1 = (uint32_t)min(n0 / kFp8Block + (GU ? 0 : 1), last) * A.nkb + kb_lo;
+        float a0 = A.xs[x0], a1 = A.xs[x1];
+        for (int i = 0; i < steps; i++, it++) {
+          const float b0 = A.w0.s[w0 + i], b1 = (GU ? A.w1.s : A.w0.s)[w1 + i];
+          if (i + 1 < steps) {
+            x0++;
+            x1++;
+          }
+          const float na0 = A.xs[x0], na1 = A.xs[x1];
+          if (!(ok = gemm_wait(&(PAIR ? sfree : tfree)[it % NBUF], ((it / NBUF) & 1) ^ 1, abort_flag))) break;
+          float* dst = scales + (it % NBUF) * 2 * kBM + r;
+          dst[0] = a0 * b0;
+          dst[32] = a1 * b0;
+          if (BN == 256) {
+            dst[kBM] = a0 * b1;
+            dst[kBM + 32] = a1 * b1;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&tfull[it % NBUF]);
+          a0 = na0;
+          a1 = na1;
+        }
       }
     }
     __syncwarp();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (PAIR) {  // neither CTA's memory is in use any more
+      cluster_arrive();
+      cluster_wait();
+      if (warp == kMmaWarp) tmem_dealloc_pair(tmem, 512);
+      return;
+    }
     if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
     if (split > 1) {  // the two cluster barriers of the other warps
       cluster_arrive();
@@ -466,30 +578,20 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     const int q = warp & 3, part = warp >> 2;
     const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16);
     int it = 0;
-    bool ok = true;
-    for (int tile = first; tile < tiles && ok; tile += step) {
-      const int t0 = (tile % tiles_m) * kBM, n0 = (tile / tiles_m) * NB;
+    bool ok = true;  // after an expired wait the barriers are kept, the work is not
+    for (int tile = first; tile < tiles; tile += step) {
+      const int t0 = (tile % tiles_m * (PAIR ? 2 : 1) + half) * kBM, n0 = (tile / tiles_m) * NB;
       const int t = t0 + 32 * q + lane;
       const bool rows_in = t0 + 32 * q < A.T;  // some row of this warp exists
-      // the weight block of this warp's columns (past the last: any, its columns are not stored)
-      const int wb = min((n0 + (BN == 256 && !GU ? part * NC : 0)) / kFp8Block, (A.rows - 1) / kFp8Block);
-      const float* ws = A.w0.s + (int64_t)wb * A.nkb + kb_lo;
-      const float* us = A.w1.s + (int64_t)wb * A.nkb + kb_lo;
-      const float* xs = A.xs + (int64_t)min(t, A.T - 1) * A.nkb + kb_lo;
       uint64_t acc[NC / 2];
 #pragma unroll
       for (int c = 0; c < NC / 2; c++) acc[c] = 0;
-      float xn = xs[0], wn = ws[0], un = GU ? us[0] : 0.f;
       for (int i = 0; i < steps; i++, it++) {
         const int b = it % NBUF;
-        const uint64_t sw = twice(xn * wn), su = GU ? twice(xn * un) : sw;
-        if (i + 1 < steps) {
-          xn = xs[i + 1];
-          wn = ws[i + 1];
-          if (GU) un = us[i + 1];
-        }
-        if (!(ok = gemm_wait(&tfull[b], (it / NBUF) & 1, abort_flag))) break;
+        if (!(ok = ok && gemm_wait(&tfull[b], (it / NBUF) & 1, abort_flag))) continue;
         tc_fence_after();
+        const float* sc = scales + b * 2 * kBM + 32 * q + lane;
+        const uint64_t sw = twice(sc[BN == 256 && !GU && part >= 2 ? kBM : 0]), su = GU ? twice(sc[kBM]) : sw;
         if (rows_in) {
           const uint32_t col = lanes + b * BN + (GU ? part * 32 : part * NC);
 #pragma unroll
@@ -503,9 +605,15 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&tfree[b]);
+        if (lane == 0) {  // the accumulator and its scales are free
+          if (PAIR) {
+            mbar_arrive_peer(peer_smem(&tfree[b], 0));
+            mbar_arrive(&sfree[b]);
+          } else {
+            mbar_arrive(&tfree[b]);
+          }
+        }
       }
-      if (!ok) break;
       if (split > 1) {
         // All MMAs have read their operands: the ring takes the accumulators.
         if (rows_in) {
@@ -585,6 +693,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
+  if (PAIR) {
+    cluster_arrive();
+    cluster_wait();
+  }
   if (split == 1) return;
 
   cluster_arrive();
@@ -695,7 +807,7 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
 #pragma unroll
           for (int j = 0; j < 4; j++)
             mma_ss_e4m3(tmem + (b * M + m) * TN, dw + (uint32_t)(m * 128 * kFp8Block / 16) + 2u * j, dx + 2u * j,
-                        idesc_e4m3_m128(TN), j != 0);
+                        idesc_e4m3(128, TN), j != 0);
         tc_commit(&tfull[b]);
         tc_commit(&empty[s]);
       }
@@ -861,12 +973,13 @@ int pick_split(int64_t tiles, int nkb, int at_once) {
   return best;
 }
 
-template <int BN, bool GU>
+template <int BN, bool GU, bool PAIR>
 int launch_gemm(const Fp8Args& a, int num_sms, cudaStream_t st) {
-  const int tiles_m = (a.T + kBM - 1) / kBM, nb = GU ? 128 : BN, tiles_n = (a.rows + nb - 1) / nb;
+  constexpr int bm = PAIR ? 2 * kBM : kBM;
+  const int tiles_m = (a.T + bm - 1) / bm, nb = GU ? 128 : BN, tiles_n = (a.rows + nb - 1) / nb;
   const int64_t tiles = (int64_t)tiles_m * tiles_n;
   if (tiles > 0x0fffffff) return -3;
-  auto kern = k_fp8_gemm<BN, GU>;
+  auto kern = k_fp8_gemm<BN, GU, PAIR>;
   static std::atomic<bool> checked{false};
   if (!checked.load(std::memory_order_relaxed)) {
     // the register split draws on what the launch takes: 5 x 96 for each lane of the five warpgroups
@@ -875,20 +988,22 @@ int launch_gemm(const Fp8Args& a, int num_sms, cudaStream_t st) {
     if (fa.numRegs * (kGemmThreads / 128) != 4 * kEpiRegs + kLastRegs) return -3;
     checked.store(true);
   }
-  if (allow_smem<k_fp8_gemm<BN, GU>, kGemmSmem(BN)>()) return -4;
-  const int split = pick_split<k_fp8_gemm<BN, GU>, kGemmSmem(BN), kGemmThreads>(tiles, a.nkb, num_sms);
+  if (allow_smem<k_fp8_gemm<BN, GU, PAIR>, kGemmSmem(BN, GU, PAIR)>()) return -4;
+  const int split = PAIR ? 1 : pick_split<k_fp8_gemm<BN, GU, PAIR>, kGemmSmem(BN, GU, PAIR), kGemmThreads>(tiles, a.nkb, num_sms);
   if (split < 1) return split;
   CUtensorMap mx, m0, m1;
   if (make_e4m3_map(&mx, a.xq, a.T, a.cols, kBM) || make_e4m3_map(&m0, a.w0.q, a.rows, a.cols, 128)) return -4;
   if (GU ? make_e4m3_map(&m1, a.w1.q, a.rows, a.cols, 128) != 0 : (m1 = m0, false)) return -4;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(split > 1 ? tiles * split : std::min<int64_t>(tiles, num_sms)));
+  cfg.gridDim = dim3((unsigned)(PAIR        ? 2 * std::min<int64_t>(tiles, num_sms / 2)
+                                : split > 1 ? tiles * split
+                                            : std::min<int64_t>(tiles, num_sms)));
   cfg.blockDim = dim3(kGemmThreads);
-  cfg.dynamicSmemBytes = kGemmSmem(BN);
+  cfg.dynamicSmemBytes = kGemmSmem(BN, GU, PAIR);
   cfg.stream = st;
-  cudaLaunchAttribute at[2] = {pdl(), cluster_of(split)};
+  cudaLaunchAttribute at[2] = {pdl(), cluster_of(PAIR ? 2 : split)};
   cfg.attrs = at;
-  cfg.numAttrs = split > 1 ? 2 : 1;
+  cfg.numAttrs = PAIR || split > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, mx, m0, m1, a, tiles_m, (int)tiles, split) == cudaSuccess ? 0 : -4;
 }
 
@@ -937,9 +1052,14 @@ int launch_fp8_product(const Fp8Args& a, bool gate_up, cudaStream_t st, int num_
     if (gate_up) return a.T <= 16 ? launch_skinny<true, 16>(a, num_sms, st) : launch_skinny<true, 32>(a, num_sms, st);
     return a.T <= 16 ? launch_skinny<false, 16>(a, num_sms, st) : launch_skinny<false, 32>(a, num_sms, st);
   }
-  if (gate_up) return launch_gemm<256, true>(a, num_sms, st);
-  const int64_t tiles = (int64_t)((a.T + kBM - 1) / kBM) * ((a.rows + 255) / 256);
-  return tiles >= num_sms ? launch_gemm<256, false>(a, num_sms, st) : launch_gemm<128, false>(a, num_sms, st);
+  // Pairs of CTAs where their tiles occupy a third of the SMs or more: at 4096 x
+  // 4096 weights 1024 tokens (64 tiles) take 22.8 us by pairs and 27.3 us by
+  // single CTAs, 512 tokens (32 tiles) 21.9 and 15.5 us.
+  const int cols = gate_up ? 128 : 256;
+  const int64_t pairs = (int64_t)((a.T + 255) / 256) * ((a.rows + cols - 1) / cols);
+  if (pairs * 3 >= num_sms)
+    return gate_up ? launch_gemm<256, true, true>(a, num_sms, st) : launch_gemm<256, false, true>(a, num_sms, st);
+  return gate_up ? launch_gemm<256, true, false>(a, num_sms, st) : launch_gemm<128, false, false>(a, num_sms, st);
 }
 
 int read_fp8_status(cudaStream_t st, int32_t* out) {

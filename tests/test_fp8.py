@@ -173,7 +173,9 @@ def check_linear(T, rows, cols, dtype, add, seed=0):
 
 SIZES = [(1, 16, 16), (1, 1, 128), (1, 4096, 2048), (2, 100, 144), (8, 256, 4096), (9, 33, 272), (16, 2048, 1008),
          (17, 128, 128), (17, 20, 16), (33, 1000, 2064), (64, 512, 4096), (127, 129, 400), (128, 128, 256), (129, 257, 1040),
-         (200, 4096, 512), (333, 1000, 2064), (700, 4100, 384), (1300, 2050, 272), (2500, 2048, 128)]
+         (200, 4096, 512), (333, 1000, 2064), (700, 4100, 384), (1300, 2050, 272), (2500, 2048, 128), (4000, 1301, 272), (2900, 2100, 400),
+         (8200, 700, 144), (513, 8192, 656),
+         (3900, 800, 1040)]
 
 
 @pytest.mark.gpu
@@ -251,7 +253,7 @@ def check_h(T, inter, cols, seed=0):
 @pytest.mark.gpu
 @pytest.mark.parametrize("T,inter,cols", [(1, 16, 16), (1, 128, 128), (1, 2048, 4096), (3, 144, 272), (8, 512, 1008),
                                           (9, 2048, 512), (16, 272, 4096), (17, 128, 128), (17, 16, 16), (40, 2048, 2064),
-                                          (128, 256, 1024), (130, 400, 640), (333, 1040, 272), (1500, 2048, 256)])
+                                          (128, 256, 1024), (130, 400, 640), (333, 1040, 272), (1500, 2048, 256), (2700, 1040, 272), (1025, 2000, 1040)])
 def test_gate_up(T, inter, cols):
     *ops, q, s = check_h(T, inter, cols)
     a, b = B.iqk_fp8_gate_up(*ops)
