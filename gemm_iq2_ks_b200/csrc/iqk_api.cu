@@ -547,14 +547,18 @@ namespace {
 int check_fp8(const uint8_t* wq, const float* ws) {
   return wq && ws && aligned(wq, 16) && aligned(ws, 4) ? IQK_OK : IQK_EINVAL;
 }
-constexpr int kFp8MaxT = 65536;
+// Limits of the products: token count, and what their kernels index with 32 bits.
+bool fp8_too_large(int32_t T, int32_t rows, int32_t cols) {
+  const int64_t nkb = fp8_blocks(cols), lim = (int64_t)1 << 31;
+  return T > 65536 || rows > 1 << 30 || T * nkb >= lim || (((int64_t)rows + 127) / 128 + 1) * nkb >= lim;
+}
 }  // namespace
 
 extern "C" int iqk_fp8_linear(const uint8_t* wq, const float* ws, int32_t rows, int32_t cols, const uint8_t* xq,
                               const float* xs, int32_t T, const void* add, void* y, int32_t y_dtype, void* stream) {
   if (T < 0 || (y_dtype != IQK_F32 && y_dtype != IQK_BF16)) return IQK_EINVAL;
   if (rows < 1 || cols < 16 || cols % 16) return IQK_ESHAPE;
-  if (T > kFp8MaxT) return IQK_EUNSUPPORTED;
+  if (fp8_too_large(T, rows, cols)) return IQK_EUNSUPPORTED;
   int rc;
   if ((rc = check_fp8(wq, ws))) return rc;
   if (T == 0) return IQK_OK;
@@ -583,7 +587,7 @@ extern "C" int iqk_fp8_gate_up(const uint8_t* gate_q, const float* gate_s, const
                                float* hs, void* stream) {
   if (T < 0) return IQK_EINVAL;
   if (inter < 16 || inter % 16 || cols < 16 || cols % 16) return IQK_ESHAPE;
-  if (T > kFp8MaxT) return IQK_EUNSUPPORTED;
+  if (fp8_too_large(T, inter, cols)) return IQK_EUNSUPPORTED;
   int rc;
   if ((rc = check_fp8(gate_q, gate_s)) || (rc = check_fp8(up_q, up_s))) return rc;
   if (T == 0) return IQK_OK;

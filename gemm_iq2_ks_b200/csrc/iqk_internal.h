@@ -169,7 +169,7 @@ int launch_topk(TopkArgs a, bool bf16, cudaStream_t st);
 
 // ------------------------------------------------------- 8-bit block-scaled
 constexpr int kFp8Block = 128;  // columns of an activation scale, rows and columns of a weight scale
-inline int fp8_blocks(int n) { return (n + kFp8Block - 1) / kFp8Block; }
+inline int fp8_blocks(int n) { return n / kFp8Block + (n % kFp8Block != 0); }
 int launch_fp8_quantize(const uint16_t* x, int64_t stride, int T, int cols, uint8_t* q, float* s, cudaStream_t st,
                         int num_sms);
 struct Fp8Mat {

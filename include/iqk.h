@@ -530,8 +530,8 @@ int iqk_fp8_quantize(const uint16_t* x, int64_t row_stride, int32_t T, int32_t c
  *   xq: device e4m3 [T][cols], xs: device float32 [T][ceil(cols / 128)], as iqk_fp8_quantize writes them
  *   add: NULL, or device [T][rows] of y's type; may be y itself
  *   y: device bf16 or float32 (y_dtype) [T][rows], written completely
- * rows >= 1, cols a positive multiple of 16, T <= 65536; wq and xq 16-byte
- * aligned. float32 accumulation, one rounding to y's type; the order of the
+ * rows >= 1, cols a positive multiple of 16, T <= 65536, rows <= 2^30, fewer
+ * than 2^31 scales in each operand; wq and xq 16-byte aligned. float32 accumulation, one rounding to y's type; the order of the
  * sums depends on the sizes only, so equal calls give equal results.
  */
 int iqk_fp8_linear(const uint8_t* wq, const float* ws, int32_t rows, int32_t cols, const uint8_t* xq, const float* xs,
@@ -544,7 +544,8 @@ int iqk_fp8_linear(const uint8_t* wq, const float* ws, int32_t rows, int32_t col
  *   float32 values, 448 h / m in float32 arithmetic): hq e4m3 [T][inter], hs
  *   float32 [T][ceil(inter / 128)], the operands of the down product.
  * gate, up: [inter][cols] each; inter and cols positive multiples of 16; hq
- * 16-byte aligned. The outputs must not overlap the inputs.
+ * 16-byte aligned; limits as iqk_fp8_linear. The outputs must not overlap the
+ * inputs.
  */
 int iqk_fp8_gate_up(const uint8_t* gate_q, const float* gate_s, const uint8_t* up_q, const float* up_s, int32_t inter,
                     int32_t cols, const uint8_t* xq, const float* xs, int32_t T, uint8_t* hq, float* hs, void* stream);

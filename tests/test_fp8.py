@@ -275,6 +275,38 @@ def test_gate_up_zero_and_not_finite_rows(T):
     assert torch.isnan(B.iqk_fp8_linear(*operand(4, 32, 256, 128), q, s)[1]).all()
 
 
+@pytest.mark.gpu
+def test_no_tokens():
+    wq, ws = operand(1, 64, 256, 128)
+    xq, xs = operand(2, 4, 256, 1)
+    assert B.iqk_fp8_linear(wq, ws, xq[:0], xs[:0]).shape == (0, 64)
+    q, s = B.iqk_fp8_gate_up(wq, ws, wq, ws, xq[:0], xs[:0])
+    assert q.shape == (0, 64) and s.shape == (0, 1)
+    q, s = B.iqk_fp8_quantize(torch.zeros((0, 256), dtype=torch.bfloat16, device="cuda"))
+    assert q.shape == (0, 256) and s.shape == (0, 2)
+
+
+@pytest.mark.gpu
+def test_offsets_past_32_bits():
+    """More than 2^31 elements behind the first row: of y, and of x and q."""
+    T, rows, cols = 65536, 33000, 16
+    wq, ws = operand(1, rows, cols, 128)
+    xq, xs = operand(2, T, cols, 1)
+    y = B.iqk_fp8_linear(wq, ws, xq, xs)
+    assert y.numel() > 2 ** 31
+    at = torch.tensor([0, 1, 40000, 65080, 65081, 65534, 65535], device="cuda")  # 2^31 elements end in row 65075
+    ref, _, tol = product(wq, ws, xq[at.cpu()].contiguous(), xs[at.cpu()].contiguous())
+    assert ((y[at].double() - ref).abs() <= tol * (1 + 2.0 ** -8) + 2.0 ** -8 * ref.abs()).all()
+    del y
+    T, cols = 140000, 16384
+    x = torch.zeros((T, cols), dtype=torch.bfloat16, device="cuda")
+    at = torch.tensor([0, 131071, 131072, 139999], device="cuda")
+    x[at] = activations(5, len(at), cols)
+    q, s = B.iqk_fp8_quantize(x)
+    same_codes(x[at], q.view(torch.uint8)[at].view(E4M3), s[at])
+    assert not q.view(torch.uint8)[1000].any()
+
+
 # ------------------------------------------------------------------ refusals
 
 def test_refusals_on_the_host():
@@ -298,7 +330,9 @@ def test_refusals_on_the_host():
                dict(ws=P + 2), dict(xs=P + 2), dict(y=P + 1), dict(add=P + 1), dict(y=P + 2, dt=0), dict(dt=2), dict(T=-1)):
         assert linear(**kw) == B.IQK_EINVAL, kw
     assert linear(rows=0) == linear(cols=0) == linear(cols=100) == B.IQK_ESHAPE
-    assert linear(T=65537) == B.IQK_EUNSUPPORTED
+    assert linear(T=65537) == linear(rows=2 ** 30 + 1) == B.IQK_EUNSUPPORTED
+    assert linear(T=65536, cols=2 ** 23) == linear(rows=2 ** 26, cols=2 ** 20) == B.IQK_EUNSUPPORTED
+    assert linear(cols=2 ** 31 - 16, T=200) == B.IQK_EUNSUPPORTED
     assert linear(T=0, xq=None, xs=None, y=None) == B.IQK_OK
 
     def gate_up(gq=P, gs=P, uq=P, us=P, inter=64, cols=256, xq=P, xs=P, T=2, hq=P, hs=P):

@@ -195,6 +195,16 @@ def test_many_tokens():
     assert ((p.double() - ref).abs() <= 96 * 2.0 ** -24 * ref).all()
 
 
+@pytest.mark.gpu
+def test_rows_past_32_bit_offsets():
+    """Rows 2^23 elements apart, the last ones more than 2^31 elements behind the first."""
+    T, E, stride = 300, 64, 1 << 23
+    flat = torch.empty((T * stride,), dtype=torch.bfloat16, device="cuda")
+    x = flat.as_strided((T, E), (stride, 1))
+    x.copy_(logits(4, T, E, torch.bfloat16))
+    check(x, 6, "far rows")
+
+
 def test_refusals_on_the_host():
     L = B.lib()
 
