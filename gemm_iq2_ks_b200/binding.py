@@ -453,36 +453,33 @@ def iqk_set_wait_limit_ns(limit_ns: int, expire: bool = False) -> int:
 _SCORES = {"softmax": 0, "sigmoid": 1}
 
 
-def _dense(t, shape, dtype, device, what: str):
-    """t, or a new tensor where it is None: a contiguous CUDA tensor of this shape, type and device."""
-    if t is None:
-        return _empty(shape, dtype, device)
-    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
-        return t
-    raise ValueError(f"{what} must be a contiguous {dtype} {list(shape)} on {device}, got {t.dtype} "
-                     f"{list(t.shape)} on {t.device}")
+def _refuse(t, shape, dtype, at: int, what: str):
+    """Raise unless t is a contiguous tensor of this shape and type on CUDA device `at`."""
+    if not (at >= 0 and t.get_device() == at and t.dtype is dtype and t.shape == shape and t.is_contiguous()):
+        raise ValueError(f"{what} must be a contiguous {dtype} {list(shape)} on "
+                         f"{f'cuda:{at}' if at >= 0 else 'a CUDA device'}, got {t.dtype} {list(t.shape)} on {t.device}"
+                         f"{'' if t.is_contiguous() else ', not contiguous'}")
 
 
-def _row_stride(t, what: str) -> int:
+def _row_stride(t, T: int, n: int, what: str) -> int:
     """Row stride of a CUDA matrix whose rows are contiguous."""
-    if not t.is_cuda or t.dim() != 2:
-        raise ValueError(f"{what} must be a CUDA tensor of two dimensions")
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor")
     stride, one = t.stride()
-    T, n = t.shape
     if one != 1 and n > 1 and T > 0:
         raise ValueError(f"{what} must have contiguous rows")
     return stride if T > 1 else n
 
 
-def _launch(fn, what: str, device, stream, *args) -> None:
-    """Call an entry point on the tensors' device."""
+def _on(at: int, fn, what: str, stream, *args) -> None:
+    """Call an entry point on CUDA device `at`, whichever is current."""
     torch = _torch()
-    C, at = torch._C, device.index
-    if C._cuda_getDevice() != at:
+    C = torch._C
+    if C._cuda_getDevice() == at:
+        rc = fn(*args, C._cuda_getCurrentRawStream(at) if stream is None else stream.cuda_stream)
+    else:
         with torch.cuda.device(at):
             rc = fn(*args, C._cuda_getCurrentRawStream(at) if stream is None else stream.cuda_stream)
-    else:
-        rc = fn(*args, C._cuda_getCurrentRawStream(at) if stream is None else stream.cuda_stream)
     if rc:
         _check(rc, what)
 
@@ -493,21 +490,26 @@ def iqk_moe_topk(logits, topk: int, score: str = "softmax", bias=None, groups: i
     (float32 or bfloat16, rows may be strided): (ids int32 [T, topk], p float32
     [T, topk]), what iqk_moe_decode and iqk_moe_prefill take."""
     torch = _torch()
-    stride = _row_stride(logits, "logits")
     T, E = logits.shape
-    dev, dt = logits.device, logits.dtype
+    stride = _row_stride(logits, T, E, "logits")
+    at, dt, shape = logits.get_device(), logits.dtype, (T, topk)
     bf16 = dt is torch.bfloat16
     if not bf16 and dt is not torch.float32:
         raise ValueError("logits must be float32 or bfloat16")
     kind = _SCORES.get(score)
     if kind is None:
         raise ValueError(f"unknown score {score!r} (expected one of {sorted(_SCORES)})")
-    shape = (T, topk)
-    ids = _dense(ids, shape, torch.int32, dev, "ids")
-    p = _dense(p, shape, torch.float32, dev, "p")
-    _launch(lib().iqk_moe_topk, "iqk_moe_topk", dev, stream, logits.data_ptr(), 1 if bf16 else 0, stride, T, E, topk,
-            kind, None if bias is None else _dense(bias, (E,), torch.float32, dev, "bias").data_ptr(), groups,
-            topk_groups, group_top, 1 if renorm else 0, scale, ids.data_ptr(), p.data_ptr())
+    if ids is None:
+        ids = _empty(shape, torch.int32, logits.device)
+    if p is None:
+        p = _empty(shape, torch.float32, logits.device)
+    _refuse(ids, shape, torch.int32, at, "ids")
+    _refuse(p, shape, torch.float32, at, "p")
+    if bias is not None:
+        _refuse(bias, (E,), torch.float32, at, "bias")
+        bias = bias.data_ptr()
+    _on(at, lib().iqk_moe_topk, "iqk_moe_topk", stream, logits.data_ptr(), 1 if bf16 else 0, stride, T, E, topk, kind,
+        bias, groups, topk_groups, group_top, 1 if renorm else 0, scale, ids.data_ptr(), p.data_ptr())
     return ids, p
 
 
@@ -515,37 +517,20 @@ def iqk_fp8_quantize(x, q=None, s=None, stream=None):
     """e4m3 codes and scales of bfloat16 x [T, cols] (rows may be strided), per
     row and 128 columns: (q float8_e4m3fn [T, cols], s float32 [T, ceil(cols / 128)])."""
     torch = _torch()
-    stride = _row_stride(x, "x")
     T, cols = shape = x.shape
-    dev = x.device
+    stride = _row_stride(x, T, cols, "x")
+    at, sshape = x.get_device(), (T, (cols + 127) >> 7)
     if x.dtype is not torch.bfloat16:
         raise ValueError("x must be bfloat16")
-    q = _dense(q, shape, torch.float8_e4m3fn, dev, "q")
-    s = _dense(s, (T, (cols + 127) >> 7), torch.float32, dev, "s")
-    _launch(lib().iqk_fp8_quantize, "iqk_fp8_quantize", dev, stream, x.data_ptr(), stride, T, cols, q.data_ptr(),
-            s.data_ptr())
+    if q is None:
+        q = _empty(shape, torch.float8_e4m3fn, x.device)
+    if s is None:
+        s = _empty(sshape, torch.float32, x.device)
+    _refuse(q, shape, torch.float8_e4m3fn, at, "q")
+    _refuse(s, sshape, torch.float32, at, "s")
+    _on(at, lib().iqk_fp8_quantize, "iqk_fp8_quantize", stream, x.data_ptr(), stride, T, cols, q.data_ptr(),
+        s.data_ptr())
     return q, s
-
-
-def _fp8_operands(wq, ws, xq, xs) -> None:
-    """Check weights [rows, cols] with scales per 128 x 128 block and activations
-    [T, cols] with scales per row and 128 columns."""
-    torch = _torch()
-    f8, f32, dev = torch.float8_e4m3fn, torch.float32, wq.device
-    rows, cols = wq.shape
-    T, n = xq.shape
-    nkb = (cols + 127) >> 7
-    if (n == cols and wq.dtype is f8 and xq.dtype is f8 and ws.dtype is f32 and xs.dtype is f32 and wq.is_cuda
-            and xq.device == dev and ws.device == dev and xs.device == dev
-            and ws.shape == ((rows + 127) >> 7, nkb) and xs.shape == (T, nkb)
-            and wq.is_contiguous() and ws.is_contiguous() and xq.is_contiguous() and xs.is_contiguous()):
-        return
-    if not wq.is_cuda:
-        raise ValueError("weights must be CUDA tensors")
-    _dense(wq, (rows, cols), f8, dev, "the weights")
-    _dense(ws, ((rows + 127) >> 7, nkb), f32, dev, "the weights' scales")
-    _dense(xq, (T, cols), f8, dev, "xq")
-    _dense(xs, (T, nkb), f32, dev, "xs")
 
 
 def iqk_fp8_linear(wq, ws, xq, xs, add=None, y=None, dtype=None, stream=None):
@@ -554,19 +539,27 @@ def iqk_fp8_linear(wq, ws, xq, xs, add=None, y=None, dtype=None, stream=None):
     gives them. y is bfloat16 or float32 (`dtype`; by default y's or add's type,
     else bfloat16); add has y's type and may be y."""
     torch = _torch()
-    _fp8_operands(wq, ws, xq, xs)
-    rows, cols = wq.shape
-    T, dev = xq.shape[0], wq.device
+    f8, f32, at = torch.float8_e4m3fn, torch.float32, wq.get_device()
+    rows, cols = wshape = wq.shape
+    T, nkb = xq.shape[0], (cols + 127) >> 7
+    _refuse(wq, wshape, f8, at, "wq")
+    _refuse(ws, ((rows + 127) >> 7, nkb), f32, at, "ws")
+    _refuse(xq, (T, cols), f8, at, "xq")
+    _refuse(xs, (T, nkb), f32, at, "xs")
     if dtype is None:
         dtype = y.dtype if y is not None else add.dtype if add is not None else torch.bfloat16
     bf16 = dtype is torch.bfloat16
-    if not bf16 and dtype is not torch.float32:
+    if not bf16 and dtype is not f32:
         raise ValueError("y must be bfloat16 or float32")
     shape = (T, rows)
-    y = _dense(y, shape, dtype, dev, "y")
-    _launch(lib().iqk_fp8_linear, "iqk_fp8_linear", dev, stream, wq.data_ptr(), ws.data_ptr(), rows, cols,
-            xq.data_ptr(), xs.data_ptr(), T,
-            None if add is None else _dense(add, shape, dtype, dev, "add").data_ptr(), y.data_ptr(), 1 if bf16 else 0)
+    if y is None:
+        y = _empty(shape, dtype, wq.device)
+    _refuse(y, shape, dtype, at, "y")
+    if add is not None:
+        _refuse(add, shape, dtype, at, "add")
+        add = add.data_ptr()
+    _on(at, lib().iqk_fp8_linear, "iqk_fp8_linear", stream, wq.data_ptr(), ws.data_ptr(), rows, cols, xq.data_ptr(),
+        xs.data_ptr(), T, add, y.data_ptr(), 1 if bf16 else 0)
     return y
 
 
@@ -575,17 +568,24 @@ def iqk_fp8_gate_up(gate_q, gate_s, up_q, up_s, xq, xs, q=None, s=None, stream=N
     [T, inter], s float32 [T, ceil(inter / 128)]), what iqk_fp8_linear takes as
     xq, xs for the down product."""
     torch = _torch()
-    _fp8_operands(gate_q, gate_s, xq, xs)
-    inter, cols = shape = gate_q.shape
-    T, dev = xq.shape[0], gate_q.device
-    f8, f32 = torch.float8_e4m3fn, torch.float32
-    _dense(up_q, shape, f8, dev, "up_q")
-    _dense(up_s, gate_s.shape, f32, dev, "up_s")
-    q = _dense(q, (T, inter), f8, dev, "q")
-    s = _dense(s, (T, (inter + 127) >> 7), f32, dev, "s")
-    _launch(lib().iqk_fp8_gate_up, "iqk_fp8_gate_up", dev, stream, gate_q.data_ptr(), gate_s.data_ptr(),
-            up_q.data_ptr(), up_s.data_ptr(), inter, cols, xq.data_ptr(), xs.data_ptr(), T, q.data_ptr(),
-            s.data_ptr())
+    f8, f32, at = torch.float8_e4m3fn, torch.float32, gate_q.get_device()
+    inter, cols = wshape = gate_q.shape
+    T, nkb, nhb = xq.shape[0], (cols + 127) >> 7, (inter + 127) >> 7
+    sshape, qshape, hshape = (nhb, nkb), (T, inter), (T, nhb)
+    if q is None:
+        q = _empty(qshape, f8, gate_q.device)
+    if s is None:
+        s = _empty(hshape, f32, gate_q.device)
+    _refuse(gate_q, wshape, f8, at, "gate_q")
+    _refuse(gate_s, sshape, f32, at, "gate_s")
+    _refuse(up_q, wshape, f8, at, "up_q")
+    _refuse(up_s, sshape, f32, at, "up_s")
+    _refuse(xq, (T, cols), f8, at, "xq")
+    _refuse(xs, (T, nkb), f32, at, "xs")
+    _refuse(q, qshape, f8, at, "q")
+    _refuse(s, hshape, f32, at, "s")
+    _on(at, lib().iqk_fp8_gate_up, "iqk_fp8_gate_up", stream, gate_q.data_ptr(), gate_s.data_ptr(), up_q.data_ptr(),
+        up_s.data_ptr(), inter, cols, xq.data_ptr(), xs.data_ptr(), T, q.data_ptr(), s.data_ptr())
     return q, s
 
 

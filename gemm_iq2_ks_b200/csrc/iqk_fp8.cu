@@ -40,75 +40,87 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
 // quotient of two bfloat16 numbers times 448 = 7 * 64 is either a rounding
 // border of e4m3 (a number of at most 5 significant bits) or at least 2^-13
 // of it away, because the difference 7 X 2^a - M B 2^b of integers with
-// X, M < 2^8 and B < 2^5 is not zero and one of a, b is. x * (448 / m) in
-// float32 is within 2^-23 of the quotient; rounding that to 18 significant
+// X, M < 2^8 and B < 2^5 is not zero and one of a, b is. x times the hardware's
+// reciprocal is within 2^-22 of the quotient; rounding that to 18 significant
 // bits (a step of at most 2^-17) returns a border exactly and keeps every
 // other quotient on its side. This costs two integer operations instead of a
-// division for each element.
+// division for each element: the kernel is bound by instructions (with IEEE
+// divisions for the two scales and 8 elements a lane it issued 18 for each
+// element and took 23.5 us for 8192 x 4096).
 __device__ __forceinline__ float snap18(float t) {
   return __uint_as_float((__float_as_uint(t) + 0x20u) & ~0x3fu);
 }
+// 448 / m within 2^-22, for m from 2^-100 to the largest bfloat16 number; the
+// scaling by 2^-8 keeps the reciprocal a normal number.
+__device__ __forceinline__ float quick_inverse(float m) {
+  float r;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(m * 0x1p-8f));
+  return r * 1.75f;
+}
+// m / 448 rounded to nearest for a bfloat16 m: product with the rounded
+// reciprocal and one correction (exact for all 128 mantissas).
+__device__ __forceinline__ float over_448(float m) {
+  constexpr float r = 1.0f / 448.0f;
+  const float q = m * r;
+  return fmaf(fmaf(-448.0f, q, m), r, q);
+}
 
 constexpr int kQuantThreads = 256;
-constexpr int kQuantUnroll = 2;
-constexpr int kQuantBlocks = 5;  // resident on an SM
+constexpr int kQuantLanes = 8;   // of a group of 128 columns, 16 columns (two 16-byte loads) each
+constexpr int kQuantBlocks = 8;  // resident on an SM: 17.2 us for 8192 x 4096, 6 of them 17.4, two groups a lane 17.4
 
-// 16 lanes take one group of 128 columns, 8 columns (16 bytes) each, two
-// groups at a time; the next two are on their way while these are converted.
+// A lane's next piece is on its way while the present one is converted.
 __global__ void __launch_bounds__(kQuantThreads, kQuantBlocks)
     k_fp8_quantize(const uint16_t* x, int64_t stride, int cols, int nkb, FastDiv by_nkb, int items, uint8_t* q, float* s) {
   griddep_wait();
   griddep_launch();
-  const int sub = threadIdx.x & 15;
-  const int per = gridDim.x * (kQuantThreads / 16);
-  struct Group {
-    uint4 v;
-    int64_t at;  // offset of this lane's columns in q; negative: none
+  const int sub = threadIdx.x % kQuantLanes;
+  const int per = gridDim.x * (kQuantThreads / kQuantLanes);
+  struct Piece {
+    uint4 v[2];
+    int row, col;  // col past the end: nothing there
   };
-  auto load = [&](Group (&g)[kQuantUnroll], int it0) {
+  auto load = [&](Piece& g, int it) {
+    g.row = (int)by_nkb.div((uint32_t)it);
+    g.col = it < items ? (it - g.row * nkb) * kFp8Block + sub * 16 : cols;
+    const uint4* p = reinterpret_cast<const uint4*>(x + g.row * stride + g.col);
 #pragma unroll
-    for (int u = 0; u < kQuantUnroll; u++) {
-      const int it = it0 + u * per;
-      const int row = (int)by_nkb.div((uint32_t)it), col = (it - row * nkb) * kFp8Block + sub * 8;
-      const bool in = it < items && col < cols;
-      g[u].v = make_uint4(0, 0, 0, 0);
-      if (in) g[u].v = *reinterpret_cast<const uint4*>(x + row * stride + col);
-      g[u].at = in ? (int64_t)row * cols + col : -1;
+    for (int j = 0; j < 2; j++) {
+      g.v[j] = make_uint4(0, 0, 0, 0);
+      if (g.col < cols) g.v[j] = p[j];
     }
   };
-  int it0 = blockIdx.x * (kQuantThreads / 16) + (threadIdx.x >> 4);
-  Group cur[kQuantUnroll], next[kQuantUnroll];
-  load(cur, it0);
-  for (; __any_sync(0xffffffffu, it0 < items); it0 += per * kQuantUnroll) {
-    load(next, it0 + per * kQuantUnroll);
+  int it = blockIdx.x * (kQuantThreads / kQuantLanes) + threadIdx.x / kQuantLanes;
+  Piece cur, next;
+  load(cur, it);
+  for (; __any_sync(0xffffffffu, it < items); it += per) {
+    load(next, it + per);
+    uint32_t m2 = 0, o[4];
 #pragma unroll
-    for (int u = 0; u < kQuantUnroll; u++) {
-      const uint32_t w[4] = {cur[u].v.x, cur[u].v.y, cur[u].v.z, cur[u].v.w};
-      uint32_t m2 = 0;
-#pragma unroll
-      for (int j = 0; j < 4; j++) m2 = __vmaxu2(m2, w[j] & 0x7fff7fffu);
-#pragma unroll
-      for (int d = 8; d; d >>= 1) m2 = __vmaxu2(m2, __shfl_xor_sync(0xffffffffu, m2, d));
-      const uint32_t mb = (m2 & 0xffffu) > (m2 >> 16) ? (m2 & 0xffffu) : (m2 >> 16);
-      const bool fine = mb < 0x7f80u;
-      const float most = fmaxf(__uint_as_float(mb << 16), kAmaxMin);
-      const float inv = fine ? kE4m3Max / most : 0.f;
-      float t[8];
-#pragma unroll
-      for (int j = 0; j < 4; j++) {
-        t[2 * j] = snap18(__uint_as_float(w[j] << 16) * inv);
-        t[2 * j + 1] = snap18(__uint_as_float(w[j] & 0xffff0000u) * inv);
-      }
-      uint2 o;
-      o.x = e4m3x4(t[0], t[1], t[2], t[3]);
-      o.y = e4m3x4(t[4], t[5], t[6], t[7]);
-      if (!fine) o = make_uint2(0, 0);
-      if (cur[u].at >= 0) {
-        *reinterpret_cast<uint2*>(q + cur[u].at) = o;
-        if (sub == 0) s[it0 + u * per] = fine ? most / kE4m3Max : __int_as_float(0x7fffffff);
-      }
-      cur[u] = next[u];
+    for (int j = 0; j < 2; j++) {
+      const uint4 v = cur.v[j];
+      m2 = __vmaxu2(__vmaxu2(m2, v.x & 0x7fff7fffu), v.y & 0x7fff7fffu);
+      m2 = __vmaxu2(__vmaxu2(m2, v.z & 0x7fff7fffu), v.w & 0x7fff7fffu);
     }
+#pragma unroll
+    for (int d = kQuantLanes / 2; d; d >>= 1) m2 = __vmaxu2(m2, __shfl_xor_sync(0xffffffffu, m2, d));
+    const uint32_t mb = max(m2 & 0xffff0000u, m2 << 16);
+    const bool fine = mb < 0x7f800000u;
+    const float most = fmaxf(__uint_as_float(mb), kAmaxMin);
+    const float inv = quick_inverse(most);
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+      const uint32_t a = j & 1 ? cur.v[j / 2].z : cur.v[j / 2].x;
+      const uint32_t b = j & 1 ? cur.v[j / 2].w : cur.v[j / 2].y;
+      o[j] = e4m3x4(snap18(__uint_as_float(a << 16) * inv), snap18(__uint_as_float(a & 0xffff0000u) * inv),
+                    snap18(__uint_as_float(b << 16) * inv), snap18(__uint_as_float(b & 0xffff0000u) * inv));
+      o[j] = fine ? o[j] : 0u;
+    }
+    if (cur.col < cols) {
+      *reinterpret_cast<uint4*>(q + (int64_t)cur.row * cols + cur.col) = make_uint4(o[0], o[1], o[2], o[3]);
+      if (sub == 0) s[it] = fine ? over_448(most) : __int_as_float(0x7fffffff);
+    }
+    cur = next;
   }
 }
 
@@ -156,12 +168,26 @@ __device__ __forceinline__ float magnitude(float h) {  // infinity for what is n
 // tcgen05 tiles of 128 tokens x BN weight rows (gate_up: 128 gate and 128 up
 // rows side by side). One 128-column block is one pipeline step: TMA brings
 // both operands' 128-byte rows (128-byte swizzle), four MMAs leave the block's
-// sums in one of the tensor-memory buffers, and 16 warps add them, times the two scales, to float32 accumulators
-// in registers (thread = token row; a quarter of the columns for each four
-// warps). CTAs are persistent over tiles:
+// sums in one of the tensor-memory buffers, and 16 warps add them, times the
+// two scales, to float32 accumulators in registers (thread = token row; a
+// quarter of the columns for each four warps). CTAs are persistent over tiles:
 // the copies and MMAs of the next tile run while this one is stored. With few
 // tiles the CTAs of a cluster split the blocks of one tile and add their
-// accumulators over distributed shared memory, in rank order.
+// accumulators over distributed shared memory, in rank order. With many, two
+// CTAs form a pair (PAIR, cta_group::2) on 256 tokens x 256 rows: each holds
+// its tokens and half of the weight rows, which halves what an MMA reads of
+// shared memory for its weights (128 x 256 x 32 alone took 196 cycles, of 128
+// that the tensor cores need).
+//
+// What bounds it is the hand-over of the accumulators: a step's sums have to
+// leave tensor memory before the MMAs of the second next step, 64 KB at a time
+// for each CTA. What counted there, measured at 8192 x 4096 x 4096: the token
+// scales go through shared memory (each row of a warp's direct load is a line
+// of its own: +12%), on the barrier that the step waits for anyway (a barrier
+// of their own: +20%), waits have CTA scope (cluster scope empties the L1:
+// twice the time), and no register of the loop is spilled (+10 to 20% for a few
+// bytes). 138 us on operands of small codes, 165 us (1.67 PFLOP/s) on quantised
+// normal data, which the card's power limit slows down.
 constexpr int kBM = 128;
 constexpr int kEpiWarps = 16, kTmaWarp = 16, kMmaWarp = 17, kScaleWarp = 18;  // and 19
 constexpr int kGemmThreads = 20 * 32;
@@ -717,6 +743,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 // then costs the tensor cores what its weights' bytes cost to read, where 128
 // token rows would be mostly padding. Thread = weight row; the token scales,
 // times the block's, come from a table that each warp writes for each step.
+// A latency chain bounds it (start, first copies, a few steps, the exchange in
+// the cluster): 4096 x 4096 takes 5.0 us for 1 token and 6.3 us for 32 (3.4 and
+// 2.7 TB/s), where a 64-token form took 8.2 us, no less than the tiles above,
+// and a stream over the weights with mma.sync 5.1 us for 1 and 10.9 for 16.
 constexpr int kSkinnyThreads = 6 * 32;
 constexpr int kSkinnyMaxT = 32;
 constexpr int kSkStage(bool gu, int TN) { return ((gu ? 256 : 128) + TN) * kFp8Block; }
@@ -1033,7 +1063,7 @@ int launch_skinny(const Fp8Args& a, int num_sms, cudaStream_t st) {
 int launch_fp8_quantize(const uint16_t* x, int64_t stride, int T, int cols, uint8_t* q, float* s, cudaStream_t st,
                         int num_sms) {
   const int nkb = fp8_blocks(cols), items = T * nkb;
-  const int per = kQuantThreads / 16;
+  const int per = kQuantThreads / kQuantLanes;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)std::min((items + per - 1) / per, num_sms * kQuantBlocks));
   cfg.blockDim = dim3(kQuantThreads);

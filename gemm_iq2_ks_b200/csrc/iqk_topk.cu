@@ -11,10 +11,15 @@
 // and each selected expert is one warp maximum over order-preserving integer
 // keys that carry the index in their last bits. Values that need scores are
 // formed in float32; where two of them that decide the result lie closer than
-// float32's error (or alike in the bits that the index leaves), the row is
-// selected once more with whole keys, in float64 if they are scores, so the
-// selection is that of the float64 scores for every row and the cheap
-// arithmetic serves nearly all of them.
+// float32's error (or alike in the bits that the index leaves), the
+// candidates are ordered anew from whole values, in float64 if they are
+// scores, so the selection is that of the float64 scores for every row and the
+// cheap arithmetic serves nearly all of them. Instructions bound it: about 250
+// for a row of 256, most of them on the half-rate integer pipe. 65536 rows of
+// bf16 logits take 22 us (1.7 TB/s; with one maximum for the value and one for
+// the index over whole keys 51 us), 2048 rows of grouped sigmoid routing 9.6 us,
+// one row 1.8 us. Warps that loop over rows with the next one fetched ahead were
+// slower (24.7 and 11.4 us).
 #include <algorithm>
 
 #include "iqk_device.cuh"
@@ -31,6 +36,13 @@ __device__ __forceinline__ float topk_inf() { return __int_as_float(0x7f800000);
 
 // NaN counts as -inf, -0 as +0.
 __device__ __forceinline__ float clean(float x) { return fmaxf(x, -topk_inf()) + 0.0f; }
+
+__device__ __forceinline__ uint32_t clean2(uint32_t pair) {  // of two bf16 values
+  const __nv_bfloat162 ninf = __nv_bfloat162(__ushort_as_bfloat16(0xff80), __ushort_as_bfloat16(0xff80));
+  const __nv_bfloat162 zero = __nv_bfloat162(__ushort_as_bfloat16(0), __ushort_as_bfloat16(0));
+  const __nv_bfloat162 v = __hadd2_rn(__hmax2(*reinterpret_cast<const __nv_bfloat162*>(&pair), ninf), zero);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
 
 // Order-preserving keys of clean values. 0 marks what cannot be selected (a
 // closed group, past the row's end, already taken); -inf maps above it.
@@ -362,12 +374,12 @@ __device__ __noinline__ int order_candidates(const TopkArgs& A, const char* logi
   return __shfl_sync(kFull, e, src);
 }
 
-// The two best of a lane's keys (those below `bound`).
-template <int NV>
+// The two best of a lane's keys (BOUNDED: of those below `bound`).
+template <bool BOUNDED, int NV>
 __device__ __forceinline__ void two_best(const uint32_t (&key)[NV], uint32_t bound, uint32_t& h1, uint32_t& h2) {
   uint32_t a[NV], b[NV];
 #pragma unroll
-  for (int i = 0; i < NV; i++) a[i] = key[i] < bound ? key[i] : 0u;
+  for (int i = 0; i < NV; i++) a[i] = !BOUNDED || key[i] < bound ? key[i] : 0u;
   if (NV == 1) {
     h1 = a[0];
     h2 = 0;
@@ -411,8 +423,12 @@ __global__ void __launch_bounds__(kTopkWarps * 32, NV <= 8 ? 4 : NV == 16 ? 2 : 
         const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
         for (int j = 0; j < VEC; j++) {
-          const uint32_t u = w[(BF16 ? j / 2 : j) & 3];
-          x[c * VEC + j] = clean(__uint_as_float(!BF16 ? u : (j & 1) ? (u & 0xffff0000u) : (u << 16)));
+          if (BF16) {
+            const uint32_t u = clean2(w[(j / 2) & 3]);
+            x[c * VEC + j] = __uint_as_float((j & 1) ? (u & 0xffff0000u) : (u << 16));
+          } else {
+            x[c * VEC + j] = clean(__uint_as_float(w[j & 3]));
+          }
         }
       } else {
 #pragma unroll
@@ -492,11 +508,11 @@ __global__ void __launch_bounds__(kTopkWarps * 32, NV <= 8 ? 4 : NV == 16 ? 2 : 
   // fetches its next two.
   constexpr uint32_t kRefill = 0xffffffffu;
   uint32_t h1, h2, taken = 0, got = 0;
-  two_best<NV>(key, kRefill, h1, h2);
+  two_best<false>(key, 0u, h1, h2);
   auto take = [&](int j) {
     uint32_t top = warp_max(h1);
     if (NV > 1 && top == kRefill) {
-      if (h1 == kRefill) two_best<NV>(key, taken, h1, h2);
+      if (h1 == kRefill) two_best<true>(key, taken, h1, h2);
       top = warp_max(h1);
     }
     if (lane == j) got = top;
@@ -566,7 +582,7 @@ __global__ void __launch_bounds__(kTopkWarps * 32, NV <= 8 ? 4 : NV == 16 ? 2 : 
     float total = w;  // of the first 16 lanes
 #pragma unroll
     for (int d = 8; d; d >>= 1) total += __shfl_xor_sync(kFull, total, d);
-    w = total > 0.f ? w / total : 0.f;
+    w = total > 0.f ? __fdividef(w, total) : 0.f;
   }
   if (have) {
     A.ids[t * A.topk + lane] = mine;
