@@ -186,8 +186,8 @@ __device__ __forceinline__ float magnitude(float h) {  // infinity for what is n
 // of its own: +12%), on the barrier that the step waits for anyway (a barrier
 // of their own: +20%), waits have CTA scope (cluster scope empties the L1:
 // twice the time), and no register of the loop is spilled (+10 to 20% for a few
-// bytes). 138 us on operands of small codes, 165 us (1.67 PFLOP/s) on quantised
-// normal data, which the card's power limit slows down.
+// bytes). 131 us on operands of small codes (2.10 PFLOP/s); quantised normal data
+// takes longer at the same instructions, the card's power limit slows it down.
 constexpr int kBM = 128;
 constexpr int kEpiWarps = 16, kTmaWarp = 16, kMmaWarp = 17, kScaleWarp = 18;  // and 19
 constexpr int kGemmThreads = 20 * 32;
@@ -327,6 +327,40 @@ __device__ __forceinline__ uint64_t twice(float s) {
 }
 __device__ __forceinline__ float lo_of(uint64_t v) { return __uint_as_float((uint32_t)v); }
 __device__ __forceinline__ float hi_of(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
+
+// The same for 32 columns straight from tensor memory, as one block: the loaded
+// registers stay in it, paired where they are (the separate forms copy them
+// first). One register too many for the gate_up kernels, which spill with it.
+#define IQK_FMA2(lo, hi, a) "mov.b64 p, {t" lo ", t" hi "};\n\tfma.rn.f32x2 %" a ", p, %17, %" a ";\n\t"
+__device__ __forceinline__ void ld_fma32(uint32_t taddr, uint64_t* a, uint64_t s) {
+  asm volatile(
+      "{\n\t.reg .b32 t<32>;\n\t.reg .b64 p;\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {t0, t1, t2, t3, t4, t5, t6, t7, t8, t9, t10, t11, "
+      "t12, t13, t14, t15, t16, t17, t18, t19, t20, t21, t22, t23, "
+      "t24, t25, t26, t27, t28, t29, t30, t31}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;\n\t"
+      IQK_FMA2("0", "1", "0")
+      IQK_FMA2("2", "3", "1")
+      IQK_FMA2("4", "5", "2")
+      IQK_FMA2("6", "7", "3")
+      IQK_FMA2("8", "9", "4")
+      IQK_FMA2("10", "11", "5")
+      IQK_FMA2("12", "13", "6")
+      IQK_FMA2("14", "15", "7")
+      IQK_FMA2("16", "17", "8")
+      IQK_FMA2("18", "19", "9")
+      IQK_FMA2("20", "21", "10")
+      IQK_FMA2("22", "23", "11")
+      IQK_FMA2("24", "25", "12")
+      IQK_FMA2("26", "27", "13")
+      IQK_FMA2("28", "29", "14")
+      IQK_FMA2("30", "31", "15")
+      "}"
+      : "+l"(a[0]), "+l"(a[1]), "+l"(a[2]), "+l"(a[3]), "+l"(a[4]), "+l"(a[5]), "+l"(a[6]), "+l"(a[7]),
+        "+l"(a[8]), "+l"(a[9]), "+l"(a[10]), "+l"(a[11]), "+l"(a[12]), "+l"(a[13]), "+l"(a[14]), "+l"(a[15])
+      : "r"(taddr), "l"(s));
+}
+#undef IQK_FMA2
 
 // Instruction descriptor, kind::f8f6f4: e4m3 A and B (format code 0), float32
 // accumulator, both K-major.
@@ -622,11 +656,15 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           const uint32_t col = lanes + b * BN + (GU ? part * 32 : part * NC);
 #pragma unroll
           for (int c0 = 0; c0 < NC; c0 += 32) {
-            uint32_t r[32];
-            tmem_ld32(col + (GU && c0 ? 128 : c0), r);
-            tmem_wait_ld(r);
+            if constexpr (GU) {
+              uint32_t r[32];
+              tmem_ld32(col + (c0 ? 128 : 0), r);
+              tmem_wait_ld(r);
 #pragma unroll
-            for (int c = 0; c < 16; c++) fma2(acc[c0 / 2 + c], r[2 * c], r[2 * c + 1], c0 ? su : sw);
+              for (int c = 0; c < 16; c++) fma2(acc[c0 / 2 + c], r[2 * c], r[2 * c + 1], c0 ? su : sw);
+            } else {
+              ld_fma32(col + c0, acc + c0 / 2, sw);
+            }
           }
         }
         tc_fence_before();
