@@ -184,10 +184,11 @@ __device__ __forceinline__ float magnitude(float h) {  // infinity for what is n
 // for each CTA. What counted there, measured at 8192 x 4096 x 4096: the token
 // scales go through shared memory (each row of a warp's direct load is a line
 // of its own: +12%), on the barrier that the step waits for anyway (a barrier
-// of their own: +20%), waits have CTA scope (cluster scope empties the L1:
-// twice the time), and no register of the loop is spilled (+10 to 20% for a few
-// bytes). 131 us on operands of small codes (2.10 PFLOP/s); quantised normal data
-// takes longer at the same instructions, the card's power limit slows it down.
+// of their own: +20%), arrivals and waits have CTA scope (what they order is
+// tensor memory, by its own fences; cluster scope took twice the time), and no
+// register of the loop is spilled (+10 to 20% for a few bytes). 131 us on
+// operands of small codes (2.10 PFLOP/s); quantised normal data takes 153 to
+// 160 us at the same instructions, the card's power limit slows it down.
 constexpr int kBM = 128;
 constexpr int kEpiWarps = 16, kTmaWarp = 16, kMmaWarp = 17, kScaleWarp = 18;  // and 19
 constexpr int kGemmThreads = 20 * 32;

@@ -185,3 +185,47 @@ def test_weights_written_just_before_the_call_are_read(T):
     torch.cuda.synchronize()
     for i, o in enumerate(outs):
         assert torch.equal(o.view(torch.int16), (a if i % 2 == 0 else b).view(torch.int16)), i
+
+
+FIRST = """
+import sys
+import torch
+sys.path[:0] = [{root!r}, {tests!r}]
+from gemm_iq2_ks_b200 import binding as B
+import test_fp8 as F, test_topk as R
+T = int(sys.argv[1])
+wq, ws = F.operand(1, 512, 512, 128)
+xq, xs = F.operand(2, T, 512, 1)
+x, lg = F.activations(3, T, 512), R.logits(4, T, 96)
+y = torch.empty((T, 512), dtype=torch.bfloat16, device="cuda")
+q, s = torch.empty((T, 512), dtype=F.E4M3, device="cuda"), torch.empty((T, 4), device="cuda")
+h, hs = torch.empty_like(q), torch.empty_like(s)
+ids, p = torch.empty((T, 5), dtype=torch.int32, device="cuda"), torch.empty((T, 5), device="cuda")
+def run():
+    B.iqk_moe_topk(lg, 5, groups=4, topk_groups=2, ids=ids, p=p)
+    B.iqk_fp8_quantize(x, q=q, s=s)
+    B.iqk_fp8_linear(wq, ws, xq, xs, y=y)
+    B.iqk_fp8_gate_up(wq, ws, wq, ws, xq, xs, q=h, s=hs)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    run()
+g.replay()
+torch.cuda.synchronize()
+a = [t.clone() for t in (y, q.view(torch.uint8), s, h.view(torch.uint8), hs, ids, p)]
+run()
+torch.cuda.synchronize()
+assert all(torch.equal(u, v) for u, v in zip(a, (y, q.view(torch.uint8), s, h.view(torch.uint8), hs, ids, p)))
+print("captured")
+"""
+
+
+@pytest.mark.parametrize("T", [1, 20, 100, 3000])
+def test_a_process_may_capture_its_first_calls(T):
+    import os
+    import subprocess
+    import sys
+    tests = os.path.dirname(os.path.abspath(__file__))
+    code = FIRST.format(root=os.path.dirname(tests), tests=tests)
+    r = subprocess.run([sys.executable, "-c", code, str(T)], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]

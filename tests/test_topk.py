@@ -113,8 +113,10 @@ def test_groups(E, groups, topk_groups, group_top):
 @pytest.mark.gpu
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("renorm", [True, False])
-def test_masks_and_extremes(score, renorm):
-    E, k = 48, 8
+@pytest.mark.parametrize("E", [48, 256])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_masks_and_extremes(score, renorm, E, dtype):
+    k = 8
     x = logits(5, 12, E)
     x[0] = -math.inf                      # nothing left
     x[1, 3:] = -math.inf                  # fewer than k
@@ -130,10 +132,11 @@ def test_masks_and_extremes(score, renorm):
     x[10] = torch.finfo(torch.float32).max
     open_bias = bias_of(1, E)
     shut_bias = open_bias.clone()
-    shut_bias[:44] = -math.inf
-    shut_bias[45] = math.nan
+    shut_bias[:E - 4] = -math.inf
+    shut_bias[E - 3] = math.nan
     forced = open_bias.clone()
     forced[[2, 30]] = math.inf
+    x = x.to(dtype)  # the lowest float32 becomes -inf in bfloat16
     for bias in (None, open_bias, shut_bias, forced):
         check(x, k, "plain", score=score, renorm=renorm, bias=bias)
         for group_top in (1, 2):
