@@ -517,7 +517,8 @@ int iqk_moe_topk(const void* logits, int32_t dtype, int64_t row_stride, int32_t 
  *   q: device e4m3 [T][cols], 16-byte aligned: 448 x / m rounded to the nearest
  *      e4m3 number (ties to even), exactly
  * A group that holds an infinity or a NaN gets s = NaN and q = 0, so products
- * of its row are NaN. The outputs must not overlap x.
+ * of its row are NaN. At most 2^30 groups in a call (IQK_EUNSUPPORTED). The
+ * outputs must not overlap x.
  */
 int iqk_fp8_quantize(const uint16_t* x, int64_t row_stride, int32_t T, int32_t cols, uint8_t* q, float* s,
                      void* stream);

@@ -206,6 +206,21 @@ def test_linear_adds_in_place_and_repeats_bitwise(T):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T", [2, 30, 60, 2300])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_linear_outputs_at_any_element(T, dtype):
+    """y and add one element off the alignment that wide stores need."""
+    rows = 2048
+    wq, ws = operand(1, rows, 272, 128)
+    xq, xs = operand(2, T, 272, 1)
+    z = torch.randn((T * rows + 1,), generator=gen(3)).to(dtype).cuda()[1:].view(T, rows)
+    buf = torch.full((T * rows + 3,), -5.0, dtype=dtype, device="cuda")
+    a = B.iqk_fp8_linear(wq, ws, xq, xs, add=z, y=buf[1:-2].view(T, rows))
+    assert torch.equal(a, B.iqk_fp8_linear(wq, ws, xq, xs, add=z.clone()))
+    assert buf[0] == -5 and (buf[-2:] == -5).all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("T", [2, 150])
 def test_linear_nan_stays_in_its_row(T):
     wq, ws = operand(1, 64, 512, 128)
