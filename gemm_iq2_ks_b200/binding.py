@@ -122,9 +122,15 @@ def _check(rc: int, what: str) -> None:
     raise RuntimeError(msg)
 
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _stream(stream) -> ctypes.c_void_p:
@@ -453,35 +459,27 @@ def iqk_set_wait_limit_ns(limit_ns: int, expire: bool = False) -> int:
 _SCORES = {"softmax": 0, "sigmoid": 1}
 
 
-def _refuse(t, shape, dtype, at: int, what: str):
-    """Raise unless t is a contiguous tensor of this shape and type on CUDA device `at`."""
-    if not (at >= 0 and t.get_device() == at and t.dtype is dtype and t.shape == shape and t.is_contiguous()):
-        raise ValueError(f"{what} must be a contiguous {dtype} {list(shape)} on "
-                         f"{f'cuda:{at}' if at >= 0 else 'a CUDA device'}, got {t.dtype} {list(t.shape)} on {t.device}"
-                         f"{'' if t.is_contiguous() else ', not contiguous'}")
+def _explain(at: int, *tensors) -> None:
+    """Raise for the first of (tensor, shape, dtype, name) that is not a contiguous tensor on CUDA device `at`."""
+    for t, shape, dtype, what in tensors:
+        if not (at >= 0 and t.get_device() == at and t.dtype is dtype and t.shape == shape and t.is_contiguous()):
+            where = f"cuda:{at}" if at >= 0 else "a CUDA device"
+            raise ValueError(f"{what} must be a contiguous {dtype} {list(shape)} on {where}, got {t.dtype} "
+                             f"{list(t.shape)} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}")
 
 
 def _row_stride(t, T: int, n: int, what: str) -> int:
     """Row stride of a CUDA matrix whose rows are contiguous."""
-    if not t.is_cuda:
-        raise ValueError(f"{what} must be a CUDA tensor")
     stride, one = t.stride()
     if one != 1 and n > 1 and T > 0:
         raise ValueError(f"{what} must have contiguous rows")
     return stride if T > 1 else n
 
 
-def _on(at: int, fn, what: str, stream, *args) -> None:
-    """Call an entry point on CUDA device `at`, whichever is current."""
-    torch = _torch()
-    C = torch._C
-    if C._cuda_getDevice() == at:
-        rc = fn(*args, C._cuda_getCurrentRawStream(at) if stream is None else stream.cuda_stream)
-    else:
-        with torch.cuda.device(at):
-            rc = fn(*args, C._cuda_getCurrentRawStream(at) if stream is None else stream.cuda_stream)
-    if rc:
-        _check(rc, what)
+def _elsewhere(at: int, fn, *args):
+    """The call with CUDA device `at` current."""
+    with _torch().cuda.device(at):
+        return fn(*args)
 
 
 def iqk_moe_topk(logits, topk: int, score: str = "softmax", bias=None, groups: int = 1, topk_groups: int = 1,
@@ -491,25 +489,34 @@ def iqk_moe_topk(logits, topk: int, score: str = "softmax", bias=None, groups: i
     [T, topk]), what iqk_moe_decode and iqk_moe_prefill take."""
     torch = _torch()
     T, E = logits.shape
-    stride = _row_stride(logits, T, E, "logits")
     at, dt, shape = logits.get_device(), logits.dtype, (T, topk)
-    bf16 = dt is torch.bfloat16
-    if not bf16 and dt is not torch.float32:
-        raise ValueError("logits must be float32 or bfloat16")
+    stride = _row_stride(logits, T, E, "logits")
     kind = _SCORES.get(score)
-    if kind is None:
-        raise ValueError(f"unknown score {score!r} (expected one of {sorted(_SCORES)})")
+    bf16 = dt is torch.bfloat16
+    if at < 0 or kind is None or not (bf16 or dt is torch.float32):
+        raise ValueError(f"logits must be float32 or bfloat16 on a CUDA device and score one of {sorted(_SCORES)}, "
+                         f"got {dt} on {logits.device} and {score!r}")
     if ids is None:
         ids = _empty(shape, torch.int32, logits.device)
     if p is None:
         p = _empty(shape, torch.float32, logits.device)
-    _refuse(ids, shape, torch.int32, at, "ids")
-    _refuse(p, shape, torch.float32, at, "p")
+    if not (ids.dtype is torch.int32 and p.dtype is torch.float32 and ids.get_device() == p.get_device() == at
+            and ids.shape == p.shape == shape and ids.is_contiguous() and p.is_contiguous()):
+        _explain(at, (ids, shape, torch.int32, "ids"), (p, shape, torch.float32, "p"))
+    b = None
     if bias is not None:
-        _refuse(bias, (E,), torch.float32, at, "bias")
-        bias = bias.data_ptr()
-    _on(at, lib().iqk_moe_topk, "iqk_moe_topk", stream, logits.data_ptr(), 1 if bf16 else 0, stride, T, E, topk, kind,
-        bias, groups, topk_groups, group_top, 1 if renorm else 0, scale, ids.data_ptr(), p.data_ptr())
+        if not (bias.dtype is torch.float32 and bias.get_device() == at and bias.shape == (E,) and bias.is_contiguous()):
+            _explain(at, (bias, (E,), torch.float32, "bias"))
+        b = bias.data_ptr()
+    C = torch._C
+    if C._cuda_getDevice() != at:
+        return _elsewhere(at, iqk_moe_topk, logits, topk, score, bias, groups, topk_groups, group_top, renorm, scale, ids,
+                          p, stream)
+    rc = lib().iqk_moe_topk(logits.data_ptr(), 1 if bf16 else 0, stride, T, E, topk, kind, b, groups, topk_groups,
+                            group_top, 1 if renorm else 0, scale, ids.data_ptr(), p.data_ptr(),
+                            C._cuda_getCurrentRawStream(at) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "iqk_moe_topk")
     return ids, p
 
 
@@ -518,18 +525,25 @@ def iqk_fp8_quantize(x, q=None, s=None, stream=None):
     row and 128 columns: (q float8_e4m3fn [T, cols], s float32 [T, ceil(cols / 128)])."""
     torch = _torch()
     T, cols = shape = x.shape
-    stride = _row_stride(x, T, cols, "x")
     at, sshape = x.get_device(), (T, (cols + 127) >> 7)
-    if x.dtype is not torch.bfloat16:
-        raise ValueError("x must be bfloat16")
+    stride = _row_stride(x, T, cols, "x")
+    f8, f32 = torch.float8_e4m3fn, torch.float32
+    if at < 0 or x.dtype is not torch.bfloat16:
+        raise ValueError(f"x must be bfloat16 on a CUDA device, got {x.dtype} on {x.device}")
     if q is None:
-        q = _empty(shape, torch.float8_e4m3fn, x.device)
+        q = _empty(shape, f8, x.device)
     if s is None:
-        s = _empty(sshape, torch.float32, x.device)
-    _refuse(q, shape, torch.float8_e4m3fn, at, "q")
-    _refuse(s, sshape, torch.float32, at, "s")
-    _on(at, lib().iqk_fp8_quantize, "iqk_fp8_quantize", stream, x.data_ptr(), stride, T, cols, q.data_ptr(),
-        s.data_ptr())
+        s = _empty(sshape, f32, x.device)
+    if not (q.dtype is f8 and s.dtype is f32 and q.get_device() == s.get_device() == at and q.shape == shape
+            and s.shape == sshape and q.is_contiguous() and s.is_contiguous()):
+        _explain(at, (q, shape, f8, "q"), (s, sshape, f32, "s"))
+    C = torch._C
+    if C._cuda_getDevice() != at:
+        return _elsewhere(at, iqk_fp8_quantize, x, q, s, stream)
+    rc = lib().iqk_fp8_quantize(x.data_ptr(), stride, T, cols, q.data_ptr(), s.data_ptr(),
+                                C._cuda_getCurrentRawStream(at) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "iqk_fp8_quantize")
     return q, s
 
 
@@ -542,24 +556,33 @@ def iqk_fp8_linear(wq, ws, xq, xs, add=None, y=None, dtype=None, stream=None):
     f8, f32, at = torch.float8_e4m3fn, torch.float32, wq.get_device()
     rows, cols = wshape = wq.shape
     T, nkb = xq.shape[0], (cols + 127) >> 7
-    _refuse(wq, wshape, f8, at, "wq")
-    _refuse(ws, ((rows + 127) >> 7, nkb), f32, at, "ws")
-    _refuse(xq, (T, cols), f8, at, "xq")
-    _refuse(xs, (T, nkb), f32, at, "xs")
     if dtype is None:
         dtype = y.dtype if y is not None else add.dtype if add is not None else torch.bfloat16
     bf16 = dtype is torch.bfloat16
     if not bf16 and dtype is not f32:
         raise ValueError("y must be bfloat16 or float32")
-    shape = (T, rows)
+    shape, wsshape, xshape, xsshape = (T, rows), ((rows + 127) >> 7, nkb), (T, cols), (T, nkb)
     if y is None:
         y = _empty(shape, dtype, wq.device)
-    _refuse(y, shape, dtype, at, "y")
+    if not (at >= 0 and wq.dtype is f8 and xq.dtype is f8 and ws.dtype is f32 and xs.dtype is f32 and y.dtype is dtype
+            and ws.get_device() == xq.get_device() == xs.get_device() == y.get_device() == at
+            and ws.shape == wsshape and xq.shape == xshape and xs.shape == xsshape and y.shape == shape
+            and wq.is_contiguous() and ws.is_contiguous() and xq.is_contiguous() and xs.is_contiguous()
+            and y.is_contiguous()):
+        _explain(at, (wq, wshape, f8, "wq"), (ws, wsshape, f32, "ws"), (xq, xshape, f8, "xq"), (xs, xsshape, f32, "xs"),
+                 (y, shape, dtype, "y"))
+    a = None
     if add is not None:
-        _refuse(add, shape, dtype, at, "add")
-        add = add.data_ptr()
-    _on(at, lib().iqk_fp8_linear, "iqk_fp8_linear", stream, wq.data_ptr(), ws.data_ptr(), rows, cols, xq.data_ptr(),
-        xs.data_ptr(), T, add, y.data_ptr(), 1 if bf16 else 0)
+        if not (add.dtype is dtype and add.get_device() == at and add.shape == shape and add.is_contiguous()):
+            _explain(at, (add, shape, dtype, "add"))
+        a = add.data_ptr()
+    C = torch._C
+    if C._cuda_getDevice() != at:
+        return _elsewhere(at, iqk_fp8_linear, wq, ws, xq, xs, add, y, dtype, stream)
+    rc = lib().iqk_fp8_linear(wq.data_ptr(), ws.data_ptr(), rows, cols, xq.data_ptr(), xs.data_ptr(), T, a, y.data_ptr(),
+                              1 if bf16 else 0, C._cuda_getCurrentRawStream(at) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "iqk_fp8_linear")
     return y
 
 
@@ -571,21 +594,30 @@ def iqk_fp8_gate_up(gate_q, gate_s, up_q, up_s, xq, xs, q=None, s=None, stream=N
     f8, f32, at = torch.float8_e4m3fn, torch.float32, gate_q.get_device()
     inter, cols = wshape = gate_q.shape
     T, nkb, nhb = xq.shape[0], (cols + 127) >> 7, (inter + 127) >> 7
-    sshape, qshape, hshape = (nhb, nkb), (T, inter), (T, nhb)
+    sshape, xshape, xsshape, qshape, hshape = (nhb, nkb), (T, cols), (T, nkb), (T, inter), (T, nhb)
     if q is None:
         q = _empty(qshape, f8, gate_q.device)
     if s is None:
         s = _empty(hshape, f32, gate_q.device)
-    _refuse(gate_q, wshape, f8, at, "gate_q")
-    _refuse(gate_s, sshape, f32, at, "gate_s")
-    _refuse(up_q, wshape, f8, at, "up_q")
-    _refuse(up_s, sshape, f32, at, "up_s")
-    _refuse(xq, (T, cols), f8, at, "xq")
-    _refuse(xs, (T, nkb), f32, at, "xs")
-    _refuse(q, qshape, f8, at, "q")
-    _refuse(s, hshape, f32, at, "s")
-    _on(at, lib().iqk_fp8_gate_up, "iqk_fp8_gate_up", stream, gate_q.data_ptr(), gate_s.data_ptr(), up_q.data_ptr(),
-        up_s.data_ptr(), inter, cols, xq.data_ptr(), xs.data_ptr(), T, q.data_ptr(), s.data_ptr())
+    if not (at >= 0 and gate_q.dtype is f8 and up_q.dtype is f8 and xq.dtype is f8 and q.dtype is f8
+            and gate_s.dtype is f32 and up_s.dtype is f32 and xs.dtype is f32 and s.dtype is f32
+            and gate_s.get_device() == up_q.get_device() == up_s.get_device() == xq.get_device() == xs.get_device()
+            == q.get_device() == s.get_device() == at
+            and up_q.shape == wshape and gate_s.shape == up_s.shape == sshape and xq.shape == xshape
+            and xs.shape == xsshape and q.shape == qshape and s.shape == hshape
+            and gate_q.is_contiguous() and gate_s.is_contiguous() and up_q.is_contiguous() and up_s.is_contiguous()
+            and xq.is_contiguous() and xs.is_contiguous() and q.is_contiguous() and s.is_contiguous()):
+        _explain(at, (gate_q, wshape, f8, "gate_q"), (gate_s, sshape, f32, "gate_s"), (up_q, wshape, f8, "up_q"),
+                 (up_s, sshape, f32, "up_s"), (xq, xshape, f8, "xq"), (xs, xsshape, f32, "xs"), (q, qshape, f8, "q"),
+                 (s, hshape, f32, "s"))
+    C = torch._C
+    if C._cuda_getDevice() != at:
+        return _elsewhere(at, iqk_fp8_gate_up, gate_q, gate_s, up_q, up_s, xq, xs, q, s, stream)
+    rc = lib().iqk_fp8_gate_up(gate_q.data_ptr(), gate_s.data_ptr(), up_q.data_ptr(), up_s.data_ptr(), inter, cols,
+                               xq.data_ptr(), xs.data_ptr(), T, q.data_ptr(), s.data_ptr(),
+                               C._cuda_getCurrentRawStream(at) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "iqk_fp8_gate_up")
     return q, s
 
 
