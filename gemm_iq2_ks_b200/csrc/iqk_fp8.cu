@@ -491,18 +491,16 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   const int kb_lo = (int)((int64_t)A.nkb * rank / split), kb_hi = (int)((int64_t)A.nkb * (rank + 1) / split);
   const int steps = kb_hi - kb_lo;
 
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < ST; i++) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
-    }
-    for (int i = 0; i < NBUF; i++) {
-      mbar_init(&tfull[i], 3);  // the commit and the two scale warps
-      mbar_init(&tfree[i], PAIR ? 2 * kEpiWarps : kEpiWarps);
-      mbar_init(&sfree[i], kEpiWarps);
-    }
-    mbar_init(drain, 1);
-    *abort_flag = 0;
+  if (warp == 0) {  // the barriers lie one after the other, a lane for each
+    constexpr int T0 = 2 * ST, T1 = T0 + NBUF, T2 = T1 + NBUF, T3 = T2 + NBUF;
+    static_assert(T3 < 32, "barriers");
+    if (lane <= T3)
+      mbar_init(&full[lane], lane < T0    ? 1
+                             : lane < T1  ? 3  // tfull: the commit and the two scale warps
+                             : lane < T2  ? (PAIR ? 2 * kEpiWarps : kEpiWarps)
+                             : lane < T3  ? kEpiWarps
+                                          : 1);
+    if (lane == 0) *abort_flag = 0;
     fence_mbar_init();
   }
   if (warp == kTmaWarp && lane == 0) {
@@ -766,7 +764,21 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 make_float4(lo_of(acc[c]), hi_of(acc[c]), lo_of(acc[c + 1]), hi_of(acc[c + 1]));
           }
           __syncwarp();
-#pragma unroll
+          // Not unrolled in full: this code runs once a tile, and fetching it costs
+          // more than its loop (4099 x 2196 x 528: 20.1 to 18.9 us). Without vector
+          // access a lane takes a column, so that a store instruction covers two
+          // runs of 16 and not eight of every fourth element (rows 2197: 47.8 to 29.1 us).
+          if (!A.vec) {
+            const int c = lane & 15, n = n0 + part * NC + c0 + c;
+#pragma unroll 4
+            for (int r = lane >> 4; r < 32; r += 2) {
+              const float v = st[r * 16 + 4 * ((c >> 2) ^ ((r >> 1) & 3)) + (c & 3)];
+              const int64_t tr = t0 + 32 * q + r;
+              if (tr < A.T && n < A.rows) put_y(A, tr * A.rows + n, v);
+            }
+            continue;
+          }
+#pragma unroll 1
           for (int i = 0; i < 4; i++) {
             const int r = 8 * i + (lane >> 2), j = lane & 3;
             const float4 v = *reinterpret_cast<const float4*>(st + r * 16 + 4 * (j ^ ((r >> 1) & 3)));
@@ -840,17 +852,11 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
   const int kb_lo = (int)((int64_t)A.nkb * rank / split), kb_hi = (int)((int64_t)A.nkb * (rank + 1) / split);
   const int steps = kb_hi - kb_lo;
 
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < ST; i++) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
-    }
-    for (int i = 0; i < NBUF; i++) {
-      mbar_init(&tfull[i], 1);
-      mbar_init(&tfree[i], 4);
-    }
-    mbar_init(drain, 1);
-    *abort_flag = 0;
+  if (warp == 0) {  // the barriers lie one after the other, a lane for each
+    constexpr int T0 = 2 * ST + NBUF, T1 = T0 + NBUF;
+    static_assert(T1 < 32, "barriers");
+    if (lane <= T1) mbar_init(&full[lane], lane >= T0 && lane < T1 ? 4 : 1);  // tfree: four warps
+    if (lane == 0) *abort_flag = 0;
     fence_mbar_init();
   }
   if (warp == 4 && lane == 0) {
