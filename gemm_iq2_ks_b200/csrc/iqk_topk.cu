@@ -157,7 +157,10 @@ __device__ __forceinline__ float value_of_expert(const Norm<float>& n, bool sigm
 template <typename R, int NV, int VEC>
 __device__ __forceinline__ unsigned open_groups(const TopkArgs& A, const R (&v)[NV], int lane, float margin, bool& near) {
   extern __shared__ __align__(16) unsigned char topk_smem[];
-  R* row = reinterpret_cast<R*>(topk_smem) + (size_t)(threadIdx.x >> 5) * A.smem_row;
+  // A warp's row starts at the same byte for both types (room for 8 a value):
+  // the warps of a block are not in step, one may be at its float64 pass while
+  // its neighbours still read float32 values.
+  R* row = reinterpret_cast<R*>(topk_smem + (size_t)(threadIdx.x >> 5) * A.smem_row * sizeof(double));
   const float inf = topk_inf();
   __syncwarp();
 #pragma unroll
@@ -595,7 +598,7 @@ int launch_nv(const TopkArgs& a, int vec, bool bf16, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((a.T + kTopkWarps - 1) / kTopkWarps));
   cfg.blockDim = dim3(kTopkWarps * 32);
-  cfg.dynamicSmemBytes = a.groups > 1 ? (size_t)kTopkWarps * a.smem_row * 8 : 0;
+  cfg.dynamicSmemBytes = a.groups > 1 ? (size_t)kTopkWarps * a.smem_row * sizeof(double) : 0;
   cfg.stream = st;
   cudaLaunchAttribute at[1] = {};
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -187,6 +187,38 @@ def test_strides_outputs_and_streams(dtype):
     assert e.shape == (0, k) and f.shape == (0, k)
 
 
+def choice(x, k, score, bias, groups, topk_groups, group_top):
+    """reference()'s ids for many rows at once, for rows with a bias and without masks."""
+    x = x.double()
+    v = (torch.softmax(x, -1) if score == "softmax" else torch.sigmoid(x)) + bias.double()
+    T, E = v.shape
+    val = v.view(T, groups, -1).topk(group_top, -1).values.sum(-1)
+    best = torch.sort(val, dim=-1, descending=True, stable=True).indices[:, :topk_groups]
+    open_ = torch.zeros((T, groups), dtype=torch.bool, device=v.device).scatter_(1, best, True)
+    v = torch.where(open_.repeat_interleave(E // groups, 1), v, -math.inf)
+    return torch.sort(v, dim=-1, descending=True, stable=True).indices[:, :k].int()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("E,groups,off", [(160, 8, 0), (256, 8, 1), (60, 5, 0), (512, 32, 3)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_doubtful_rows_among_ordinary_ones(E, groups, off, dtype):
+    """Rows whose groups tie, which the float64 pass orders, between ordinary
+    ones: the warps of a block are then at different passes at once."""
+    T, k, n = 8192, 6, E // groups
+    wide = logits(E, T, E + 8, dtype)
+    x = wide[:, off:off + E]
+    tied = torch.rand((T,), generator=torch.Generator().manual_seed(1)).cuda() < 0.4
+    x[tied] = 0.25
+    bias = bias_of(2, n).repeat(groups)  # alike in every group
+    for group_top in (1, 2):
+        kw = dict(score="sigmoid", bias=bias, groups=groups, topk_groups=groups // 2, group_top=group_top)
+        want = choice(x, k, **kw)
+        for _ in range(5):
+            ids, _ = B.iqk_moe_topk(x, k, **kw)
+            assert torch.equal(ids, want)
+
+
 @pytest.mark.gpu
 def test_many_tokens():
     x = logits(11, 65536, 256, torch.bfloat16)
