@@ -554,6 +554,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           __syncwarp();
         }
       }
+      // The last stages' commits arrive here, too: nothing may exit before they have.
+      for (int j = it < ST ? 0 : it - ST; ok && j < it; j++) ok = gemm_wait(&empty[j % ST], (j / ST) & 1, abort_flag);
       if (!ok && half == 0)  // a wait expired: let the copies in flight land
         for (int j = it < ST ? 0 : it - ST; j < it; j++) mbar_wait_ns(&full[j % ST], (j / ST) & 1, kDrainWaitNs);
       if (!ok && half)  // these count on the other CTA's barriers: a time that copies do not take
@@ -875,9 +877,10 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
   if (warp == 4) {
     const bool leader = elect_one();
     int i = 0;
+    bool ok = true;
     for (; i < steps; i++) {
       const int s = i % ST, k = (kb_lo + i) * kFp8Block;
-      if (!gemm_wait(&empty[s], ((i / ST) & 1) ^ 1, abort_flag)) break;
+      if (!(ok = gemm_wait(&empty[s], ((i / ST) & 1) ^ 1, abort_flag))) break;
       if (leader) {
         uint8_t* a = smem + s * SB;
         mbar_arrive_expect_tx(&full[s], SB);
@@ -887,7 +890,9 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
       }
       __syncwarp();
     }
-    if (i < steps)  // a wait expired: let the copies in flight land
+    // The last stages' commits arrive here, too: nothing may exit before they have.
+    for (int j = i < ST ? 0 : i - ST; ok && j < i; j++) ok = gemm_wait(&empty[j % ST], (j / ST) & 1, abort_flag);
+    if (!ok)  // a wait expired: let the copies in flight land
       for (int j = i < ST ? 0 : i - ST; j < i; j++) mbar_wait_ns(&full[j % ST], (j / ST) & 1, kDrainWaitNs);
   } else if (warp == 5) {
     const bool leader = elect_one();

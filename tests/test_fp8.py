@@ -322,6 +322,36 @@ def test_offsets_past_32_bits():
     assert not q.view(torch.uint8)[1000].any()
 
 
+@pytest.mark.gpu
+def test_products_follow_one_another():
+    """Every product kernel right behind every other, many times over: what one
+    leaves in an SM's shared or tensor memory is complete when the next takes it."""
+    calls, alone = [], []
+    for n, (T, rows, cols, gate_up) in enumerate([(1, 1040, 1024, False), (9, 528, 272, True), (40, 1040, 1024, False),
+                                                  (40, 528, 640, True), (700, 2050, 144, False), (1300, 2050, 272, False),
+                                                  (1300, 2064, 16, True), (2600, 1040, 128, True)]):
+        wq, ws = operand(n, rows, cols, 128)
+        uq, us = operand(n + 50, rows, cols, 128)
+        xq, xs = operand(n + 100, T, cols, 1)
+        if gate_up:
+            def call(a=(wq, ws, uq, us, xq, xs)):
+                q, s = B.iqk_fp8_gate_up(*a)
+                return q.view(torch.uint8), s.view(torch.int32)
+        else:
+            def call(a=(wq, ws, xq, xs)):
+                return (B.iqk_fp8_linear(*a).view(torch.int16),)
+        calls.append(call)
+        alone.append([t.clone() for t in call()])
+        torch.cuda.synchronize()
+    order = torch.randint(0, len(calls), (40, 25), generator=gen(9)).tolist()
+    for some in order:
+        outs = [calls[i]() for i in some]
+        torch.cuda.synchronize()
+        for i, out in zip(some, outs):
+            assert all(torch.equal(a, b) for a, b in zip(out, alone[i])), i
+    assert B.iqk_fp8_status() == B.IQK_OK
+
+
 # ------------------------------------------------------------------ refusals
 
 def test_refusals_on_the_host():
