@@ -1379,7 +1379,7 @@ __global__ void __launch_bounds__(256) k_pack_slots(WDev w, int bpi, uint8_t* __
 // ================================================================== host
 
 // Bound of the data-barrier waits and the expire hook, copied into every
-// decode-side launch (iqk_set_wait_limit_ns).
+// decode-side launch and every 8-bit product (iqk_set_wait_limit_ns).
 static std::atomic<uint64_t> g_wait_ns{kDefaultWaitNs};
 static std::atomic<int> g_expire{0};
 
@@ -1387,6 +1387,8 @@ void set_wait_limit(uint64_t ns, int expire) {
   g_wait_ns.store(ns ? ns : kDefaultWaitNs);
   g_expire.store(expire ? 1 : 0);
 }
+uint64_t wait_limit_ns() { return g_wait_ns.load(); }
+bool waits_expire() { return g_expire.load() != 0; }
 
 int read_floor_status(cudaStream_t st, int32_t* out) {
   if (cudaStreamSynchronize(st) != cudaSuccess) return -4;

@@ -208,16 +208,22 @@ constexpr size_t kGemmSmem(int BN, bool gu, bool pair) {
 static_assert(kBM * kPitch(256) * 4 <= kGemmRing(256, false) && kBM * kPitch(128) * 4 <= kGemmRing(128, false),
               "accumulators");
 
-// Bounded wait: gives up after a million tries (each of which the hardware
-// suspends for a while: seconds in all), or soon after another warp of the CTA did.
-__device__ __forceinline__ bool gemm_wait(uint64_t* bar, uint32_t par, volatile uint32_t* abort_flag) {
-  for (uint32_t i = 0; i < (1u << 20); i++) {
-    if (mbar_try_wait(bar, par)) return true;
-    if (i % 256 == 255 && *abort_flag) return false;
+// Bounded wait of a whole warp: gives up, every lane alike, once `limit_ns` of
+// the GPU's global timer have passed, or soon after another warp of the CTA did.
+__device__ __forceinline__ bool gemm_wait(uint64_t* bar, uint32_t par, volatile uint32_t* abort_flag, uint64_t limit_ns) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, par))) return true;
+  const uint64_t t0 = globaltimer_ns();
+  for (;;) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, par))) return true;
+    const bool late = globaltimer_ns() - t0 >= limit_ns;
+    if (__any_sync(0xffffffffu, late || *abort_flag)) {
+      if (late) {
+        *abort_flag = 1;
+        atomicOr(&g_fp8_status, 2);
+      }
+      return false;
+    }
   }
-  *abort_flag = 1;
-  atomicOr(&g_fp8_status, 2);
-  return false;
 }
 
 template <bool PAIR = false>
@@ -257,6 +263,12 @@ __device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* m
       "[%4];" ::"r"(smem_u32(dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
       : "memory");
+}
+__device__ __forceinline__ void mbar_complete_tx(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void st_peer(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 __device__ __forceinline__ void tc_commit_pair(uint64_t* bar) {
   asm volatile(
@@ -463,6 +475,33 @@ __device__ __forceinline__ void finish_row(const Fp8Args& A, const float* src, i
   }
 }
 
+// After a wait of a pair expired, when both CTAs have stopped: lets the products
+// and the copies in flight end. The copies of both CTAs count on the first one's
+// barriers, each step's as 2 x SB bytes that the first CTA expects; where the
+// CTAs stopped at different steps (by at most the ring's depth), it accounts
+// for what is missing.
+template <int ST, int SB>
+__device__ __forceinline__ void drain_pair(uint64_t* full, uint64_t* drain, int n0, int n1, int half, bool copies,
+                                           bool products) {
+  if (products) {
+    if (half == 0 && elect_one()) tc_commit_pair(drain);
+    __syncwarp();
+    mbar_wait_ns(drain, 0, kDrainWaitNs);
+  }
+  if (copies && half == 0) {
+    const int most = max(n0, n1);
+    if (elect_one())
+      for (int j = min(n0, n1); j < most; j++) {
+        if (n0 < n1)
+          mbar_arrive_expect_tx(&full[j % ST], SB);  // the second CTA's copies alone
+        else
+          mbar_complete_tx(&full[j % ST], SB);  // copies that the second CTA did not begin
+      }
+    __syncwarp();
+    for (int j = most < ST ? 0 : most - ST; j < most; j++) mbar_wait_ns(&full[j % ST], (j / ST) & 1, kDrainWaitNs);
+  }
+}
+
 template <int BN, bool GU, bool PAIR>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     k_fp8_gemm(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap m0,
@@ -481,8 +520,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   uint64_t* tfree = tfull + NBUF;
   uint64_t* sfree = tfree + NBUF;
   uint64_t* drain = sfree + NBUF;
-  uint32_t* holder = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* never = drain + 1;  // nothing arrives on it (testing hook)
+  uint32_t* holder = reinterpret_cast<uint32_t*>(never + 1);
   volatile uint32_t* abort_flag = holder + 1;
+  volatile uint32_t* copied = holder + 2;  // PAIR: steps that each CTA has copied; the top bit: it gave up
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   // PAIR: `split` is 1 and the cluster's two CTAs take the halves of a tile's 256 tokens.
   const int rank = split > 1 ? (int)cluster_rank() : 0, half = PAIR ? (int)cluster_rank() : 0;
@@ -492,9 +533,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   const int steps = kb_hi - kb_lo;
 
   if (warp == 0) {  // the barriers lie one after the other, a lane for each
-    constexpr int T0 = 2 * ST, T1 = T0 + NBUF, T2 = T1 + NBUF, T3 = T2 + NBUF;
-    static_assert(T3 < 32, "barriers");
-    if (lane <= T3)
+    constexpr int T0 = 2 * ST, T1 = T0 + NBUF, T2 = T1 + NBUF, T3 = T2 + NBUF;  // from T3: drain, never
+    static_assert(T3 + 1 < 32 && (T3 + 2) * 8 + 16 <= 256, "barriers");
+    if (lane <= T3 + 1)
       mbar_init(&full[lane], lane < T0    ? 1
                              : lane < T1  ? 3  // tfull: the commit and the two scale warps
                              : lane < T2  ? (PAIR ? 2 * kEpiWarps : kEpiWarps)
@@ -535,7 +576,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         const int t0 = (tile % tiles_m * (PAIR ? 2 : 1) + half) * kBM, n0 = (tile / tiles_m) * NB;
         for (int i = 0; i < steps; i++, it++) {
           const int s = it % ST, k = (kb_lo + i) * kFp8Block;
-          if (!(ok = gemm_wait(&empty[s], ((it / ST) & 1) ^ 1, abort_flag))) break;
+          if (!(ok = gemm_wait(&empty[s], ((it / ST) & 1) ^ 1, abort_flag, A.wait_ns))) break;
           if (leader) {
             uint8_t* a = smem + s * SB;
             uint8_t* w = a + kBM * kFp8Block;
@@ -555,12 +596,15 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         }
       }
       // The last stages' commits arrive here, too: nothing may exit before they have.
-      for (int j = it < ST ? 0 : it - ST; ok && j < it; j++) ok = gemm_wait(&empty[j % ST], (j / ST) & 1, abort_flag);
-      if (!ok && half == 0)  // a wait expired: let the copies in flight land
+      for (int j = it < ST ? 0 : it - ST; ok && j < it; j++)
+        ok = gemm_wait(&empty[j % ST], (j / ST) & 1, abort_flag, A.wait_ns);
+      if (!ok && !PAIR)  // a wait expired: let the copies in flight land
         for (int j = it < ST ? 0 : it - ST; j < it; j++) mbar_wait_ns(&full[j % ST], (j / ST) & 1, kDrainWaitNs);
-      if (!ok && half)  // these count on the other CTA's barriers: a time that copies do not take
-        for (const uint64_t t = globaltimer_ns(); globaltimer_ns() - t < 10000000ull;) {
-        }
+      if (PAIR && leader) {  // both CTAs learn of it; see drain_pair below
+        const uint32_t v = (uint32_t)it | (ok ? 0u : 0x80000000u);
+        st_peer(peer_smem(holder + 2 + half, 0), v);
+        st_peer(peer_smem(holder + 2 + half, 1), v);
+      }
     }
     if (warp == kMmaWarp && half == 0) {
       const bool leader = elect_one();
@@ -571,8 +615,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       for (int tile = first; tile < tiles && ok; tile += step) {
         for (int i = 0; i < steps; i++, it++) {
           const int s = it % ST, b = it % NBUF;
-          if (!(ok = gemm_wait(&full[s], (it / ST) & 1, abort_flag) &&
-                     gemm_wait(&tfree[b], ((it / NBUF) & 1) ^ 1, abort_flag)))
+          if (!(ok = gemm_wait(&full[s], (it / ST) & 1, abort_flag, A.wait_ns) &&
+                     gemm_wait(&tfree[b], ((it / NBUF) & 1) ^ 1, abort_flag, A.wait_ns)))
             break;
           tc_fence_after();
           if (leader) {
@@ -591,13 +635,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           __syncwarp();
         }
       }
-      if (!ok) {  // a wait expired: let the products in flight end before their tensor memory is given back
-        if (leader) {
-          if (PAIR)
-            tc_commit_pair(drain);
-          else
-            tc_commit(drain);
-        }
+      if (!ok && !PAIR) {  // a wait expired: let the products in flight end before their tensor memory is given back
+        if (leader) tc_commit(drain);
         mbar_wait_ns(drain, 0, kDrainWaitNs);
       }
     }
@@ -620,7 +659,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             x1++;
           }
           const float na0 = A.xs[x0], na1 = A.xs[x1];
-          if (!(ok = gemm_wait(&(PAIR ? sfree : tfree)[it % NBUF], ((it / NBUF) & 1) ^ 1, abort_flag))) break;
+          if (!(ok = gemm_wait(&(PAIR ? sfree : tfree)[it % NBUF], ((it / NBUF) & 1) ^ 1, abort_flag, A.wait_ns)))
+            break;
           float* dst = scales + (it % NBUF) * 2 * kBM + r;
           dst[0] = a0 * b0;
           dst[32] = a1 * b0;
@@ -642,6 +682,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     if (PAIR) {  // neither CTA's memory is in use any more
       cluster_arrive();
       cluster_wait();
+      if ((copied[0] | copied[1]) >> 31) {
+        drain_pair<ST, SB>(full, drain, copied[0] & 0x7fffffffu, copied[1] & 0x7fffffffu, half,
+                           warp == kTmaWarp, warp == kMmaWarp);
+        cluster_arrive();
+        cluster_wait();
+      }
       if (warp == kMmaWarp) tmem_dealloc_pair(tmem, 512);
       return;
     }
@@ -662,6 +708,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16);
     int it = 0;
     bool ok = true;  // after an expired wait the barriers are kept, the work is not
+    if (A.expire && warp == 0) ok = gemm_wait(never, 0, abort_flag, A.wait_ns);  // testing hook: this wait runs out
     for (int tile = first; tile < tiles; tile += step) {
       const int t0 = (tile % tiles_m * (PAIR ? 2 : 1) + half) * kBM, n0 = (tile / tiles_m) * NB;
       const int t = t0 + 32 * q + lane;
@@ -671,7 +718,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       for (int c = 0; c < NC / 2; c++) acc[c] = 0;
       for (int i = 0; i < steps; i++, it++) {
         const int b = it % NBUF;
-        if (!(ok = ok && gemm_wait(&tfull[b], (it / NBUF) & 1, abort_flag))) continue;
+        if (!(ok = ok && gemm_wait(&tfull[b], (it / NBUF) & 1, abort_flag, A.wait_ns))) continue;
         tc_fence_after();
         const float* sc = scales + b * 2 * kBM + 32 * q + lane;
         const uint64_t sw = twice(sc[BN == 256 && !GU && part >= 2 ? kBM : 0]), su = GU ? twice(sc[kBM]) : sw;
@@ -703,7 +750,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       }
       if (split > 1) {
         // All MMAs have read their operands: the ring takes the accumulators.
-        if (rows_in) {
+        if (rows_in && ok) {
           float* dst = reinterpret_cast<float*>(smem) + (size_t)(32 * q + lane) * kPitch(BN);
 #pragma unroll
           for (int c = 0; c < NC; c += 4)
@@ -797,6 +844,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   if (PAIR) {
     cluster_arrive();
     cluster_wait();
+    if ((copied[0] | copied[1]) >> 31) {  // the other warps drain
+      cluster_arrive();
+      cluster_wait();
+    }
   }
   if (split == 1) return;
 
@@ -846,7 +897,8 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
   uint64_t* tfull = empty + ST;
   uint64_t* tfree = tfull + NBUF;
   uint64_t* drain = tfree + NBUF;
-  uint32_t* holder = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* never = drain + 1;  // nothing arrives on it (testing hook)
+  uint32_t* holder = reinterpret_cast<uint32_t*>(never + 1);
   volatile uint32_t* abort_flag = holder + 1;
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const int rank = split > 1 ? (int)cluster_rank() : 0;
@@ -856,8 +908,8 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
 
   if (warp == 0) {  // the barriers lie one after the other, a lane for each
     constexpr int T0 = 2 * ST + NBUF, T1 = T0 + NBUF;
-    static_assert(T1 < 32, "barriers");
-    if (lane <= T1) mbar_init(&full[lane], lane >= T0 && lane < T1 ? 4 : 1);  // tfree: four warps
+    static_assert(T1 + 1 < 32 && (T1 + 2) * 8 + 8 <= 256, "barriers");
+    if (lane <= T1 + 1) mbar_init(&full[lane], lane >= T0 && lane < T1 ? 4 : 1);  // tfree: four warps
     if (lane == 0) *abort_flag = 0;
     fence_mbar_init();
   }
@@ -880,7 +932,7 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
     bool ok = true;
     for (; i < steps; i++) {
       const int s = i % ST, k = (kb_lo + i) * kFp8Block;
-      if (!(ok = gemm_wait(&empty[s], ((i / ST) & 1) ^ 1, abort_flag))) break;
+      if (!(ok = gemm_wait(&empty[s], ((i / ST) & 1) ^ 1, abort_flag, A.wait_ns))) break;
       if (leader) {
         uint8_t* a = smem + s * SB;
         mbar_arrive_expect_tx(&full[s], SB);
@@ -891,7 +943,8 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
       __syncwarp();
     }
     // The last stages' commits arrive here, too: nothing may exit before they have.
-    for (int j = i < ST ? 0 : i - ST; ok && j < i; j++) ok = gemm_wait(&empty[j % ST], (j / ST) & 1, abort_flag);
+    for (int j = i < ST ? 0 : i - ST; ok && j < i; j++)
+      ok = gemm_wait(&empty[j % ST], (j / ST) & 1, abort_flag, A.wait_ns);
     if (!ok)  // a wait expired: let the copies in flight land
       for (int j = i < ST ? 0 : i - ST; j < i; j++) mbar_wait_ns(&full[j % ST], (j / ST) & 1, kDrainWaitNs);
   } else if (warp == 5) {
@@ -900,7 +953,9 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
     int i = 0;
     for (; i < steps; i++) {
       const int s = i % ST, b = i % NBUF;
-      if (!gemm_wait(&full[s], (i / ST) & 1, abort_flag) || !gemm_wait(&tfree[b], ((i / NBUF) & 1) ^ 1, abort_flag)) break;
+      if (!gemm_wait(&full[s], (i / ST) & 1, abort_flag, A.wait_ns) ||
+          !gemm_wait(&tfree[b], ((i / NBUF) & 1) ^ 1, abort_flag, A.wait_ns))
+        break;
       tc_fence_after();
       if (leader) {
         const uint64_t dw = d0 + (uint32_t)(s * (SB / 16)), dx = dw + M * 128 * kFp8Block / 16;
@@ -933,7 +988,8 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
       for (int c = 0; c < TN / 2; c++) acc[m][c] = 0;
     float xn = xs[0], wn = ws[0], un = GU ? us[0] : 0.f;
     bool ok = true;
-    for (int i = 0; i < steps; i++) {
+    if (A.expire && warp == 0) ok = gemm_wait(never, 0, abort_flag, A.wait_ns);  // testing hook: this wait runs out
+    for (int i = 0; ok && i < steps; i++) {
       const int b = i % NBUF;
       __syncwarp();
       tab[lane] = xn * wn;
@@ -944,7 +1000,7 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
         if (GU) un = us[i + 1];
       }
       __syncwarp();
-      if (!(ok = gemm_wait(&tfull[b], (i / NBUF) & 1, abort_flag))) break;
+      if (!(ok = gemm_wait(&tfull[b], (i / NBUF) & 1, abort_flag, A.wait_ns))) break;
       tc_fence_after();
 #pragma unroll
       for (int m = 0; m < M; m++)
@@ -1148,7 +1204,9 @@ int launch_fp8_quantize(const uint16_t* x, int64_t stride, int T, int cols, uint
              : -4;
 }
 
-int launch_fp8_product(const Fp8Args& a, bool gate_up, cudaStream_t st, int num_sms) {
+int launch_fp8_product(Fp8Args a, bool gate_up, cudaStream_t st, int num_sms) {
+  a.wait_ns = wait_limit_ns();
+  a.expire = waits_expire();
   if (a.T <= kSkinnyMaxT) {
     if (gate_up) return a.T <= 16 ? launch_skinny<true, 16>(a, num_sms, st) : launch_skinny<true, 32>(a, num_sms, st);
     return a.T <= 16 ? launch_skinny<false, 16>(a, num_sms, st) : launch_skinny<false, 32>(a, num_sms, st);

@@ -115,11 +115,13 @@ int launch_floor(const WDev& w, int fmt, const int32_t* experts, int n, uint32_t
 // The floor's timeout flag (cleared by every floor call), after syncing `st`.
 int read_floor_status(cudaStream_t st, int32_t* out);
 
-// Bound of the decode-side kernels' data-barrier waits in ns (0: the
-// default), and the expire hook (warp 0 of every CTA also waits on a barrier
-// nothing arrives on), applied to launches made from now on.
+// Bound of the waits of the decode-side kernels and the 8-bit products in ns
+// (0: the default), and the expire hook (warp 0 of every CTA also waits on a
+// barrier nothing arrives on), applied to launches made from now on.
 constexpr uint64_t kDefaultWaitNs = 2000000000ull;
 void set_wait_limit(uint64_t ns, int expire);
+uint64_t wait_limit_ns();
+bool waits_expire();
 
 // ----------------------------------------------------------------- prefill
 struct PrefillWs {
@@ -186,8 +188,11 @@ struct Fp8Args {
   int32_t T, rows, cols, nkb;
   bool f32;
   bool vec;  // rows, y and add allow accesses of four elements
+  // set by launch_fp8_product
+  bool expire;
+  uint64_t wait_ns;
 };
-int launch_fp8_product(const Fp8Args& a, bool gate_up, cudaStream_t st, int num_sms);
+int launch_fp8_product(Fp8Args a, bool gate_up, cudaStream_t st, int num_sms);
 // Whether a bounded wait of a product expired since the last call (cleared), after syncing `st`.
 int read_fp8_status(cudaStream_t st, int32_t* out);
 

@@ -453,11 +453,11 @@ int iqk_floor_status(void* stream);
 
 /*
  * iqk_set_wait_limit_ns -- the bound of the device-side waits of the decode,
- * GEMV, switch-linear (decode mode) and floor kernels launched from now on,
- * in nanoseconds of the GPU's global timer (0 restores the default, 2 s).
- * A wait that runs out sets the call's status to IQK_ETIMEOUT
- * (iqk_moe_status, iqk_floor_status); the kernel then lets its copies in
- * flight land (bounded separately, 2 s) and finishes without further loads,
+ * GEMV, switch-linear (decode mode), floor and 8-bit product kernels launched
+ * from now on, in nanoseconds of the GPU's global timer (0 restores the
+ * default, 2 s). A wait that runs out sets the call's status to IQK_ETIMEOUT
+ * (iqk_moe_status, iqk_floor_status, iqk_fp8_status); the kernel then lets its
+ * copies and tensor-core products in flight end (bounded separately, 2 s) and finishes without further loads,
  * and the call's outputs are incomplete.
  * expire != 0 is a testing hook: warp 0 of every CTA of those kernels then
  * also waits once on a barrier nothing arrives on, so the bound runs out on
@@ -555,7 +555,8 @@ int iqk_fp8_gate_up(const uint8_t* gate_q, const float* gate_s, const uint8_t* u
  * iqk_fp8_status -- synchronises `stream`, then reports whether a bounded
  * device wait of an iqk_fp8_linear or iqk_fp8_gate_up call expired on the
  * current device since the last iqk_fp8_status (IQK_ETIMEOUT; that call's
- * output is incomplete), and clears it.
+ * output is incomplete), and clears it. One word per device serves all callers:
+ * a poll reports and clears what any stream's or thread's calls have left.
  */
 int iqk_fp8_status(void* stream);
 

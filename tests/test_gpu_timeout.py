@@ -94,3 +94,35 @@ def test_floor_wait_runs_out_then_recovers(B):
     assert B.iqk_floor_status() == B.IQK_OK
     assert np.array_equal(out[0], O.floor_xor(w, 2))
     assert np.array_equal(out[1], O.floor_xor(w, 0))
+
+
+@pytest.mark.parametrize("T,rows,cols,gate_up", [
+    (1, 1040, 4096, False), (3, 528, 128, False), (20, 1040, 2064, False),  # few tokens, split and not
+    (1, 528, 4096, True), (20, 16, 144, True),
+    (40, 1040, 4096, False), (40, 300, 128, False), (700, 2050, 656, False),  # tiles of single CTAs
+    (40, 528, 4096, True), (300, 272, 272, True),
+    (2600, 1100, 2064, False), (2600, 1100, 272, False),  # pairs of CTAs: longer and shorter than their ring
+    (5200, 2100, 272, False),  # several tiles for each pair
+    (2600, 1040, 2064, True)])
+def test_product_waits_run_out_then_recover(B, T, rows, cols, gate_up):
+    from tests import test_fp8 as F
+    wq, ws = F.operand(1, rows, cols, 128)
+    uq, us = F.operand(2, rows, cols, 128)
+    xq, xs = F.operand(3, T, cols, 1)
+
+    def call():
+        if gate_up:
+            q, s = B.iqk_fp8_gate_up(wq, ws, uq, us, xq, xs)
+            return q.view(torch.uint8), s.view(torch.int32)
+        return (B.iqk_fp8_linear(wq, ws, xq, xs).view(torch.int16),)
+
+    want = call()
+    assert B.iqk_fp8_status() == B.IQK_OK
+    for _ in range(2):
+        with expire_waits(B):
+            call()
+        assert B.iqk_fp8_status() == B.IQK_ETIMEOUT
+        assert B.iqk_fp8_status() == B.IQK_OK  # reported once
+        got = call()
+        assert B.iqk_fp8_status() == B.IQK_OK
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
