@@ -149,11 +149,32 @@ __device__ __forceinline__ float value_of_expert(const Norm<float>& n, bool sigm
   return x == -topk_inf() || !(b > -topk_inf()) ? -topk_inf() : v;
 }
 
+// A group's value from its best two selection values, and what float32
+// arithmetic may have moved it by, beyond the scores' own error: half a step
+// for each of the two (score + bias) and for their sum, each relative to a
+// number of at most the larger one's size, twice; so 2^-22 of that size, and
+// as much again for the comparison's own roundings. The sum itself may be far
+// smaller than the two. A sum below float32's range stays ahead of -inf.
+template <typename R>
+__device__ __forceinline__ R group_value(R b1, R b2, int group_top) {
+  const R v = b1 + (group_top == 2 && b2 > (R)-topk_inf() ? b2 : R(0));
+  return sizeof(R) == 4 && b1 > (R)-topk_inf() ? (R)fmaxf((float)v, -3.402823466e38f) : v;
+}
+__device__ __forceinline__ float group_slack(float b1, float b2, int group_top) {
+  const float m = fmaxf(fabsf(b1), group_top == 2 && b2 > -topk_inf() ? fabsf(b2) : 0.f);
+  return 0x1p-21f * fminf(m, 3.402823466e38f);
+}
+// Whether the last open group (lowest value `least`, less its slack) may not be
+// ahead of the first closed one (`most`, its slack added).
+__device__ __forceinline__ bool groups_near(float least, float most, float margin) {
+  return most > -topk_inf() && !(least - most > margin);
+}
+
 // The open groups of a row: bit g * lanes_per_group for each. v: the lane's
 // selection values. L lanes take a group, each a strided part of it from the
 // values in shared memory; then the group's best two meet by shuffles.
-// near: whether the last open group's value is within `margin` (and 2^-20 of
-// its size) of the first closed one's.
+// near: whether the last open group's value is within `margin` and both slacks
+// of the first closed one's.
 template <typename R, int NV, int VEC>
 __device__ __forceinline__ unsigned open_groups(const TopkArgs& A, const R (&v)[NV], int lane, float margin, bool& near) {
   extern __shared__ __align__(16) unsigned char topk_smem[];
@@ -185,7 +206,7 @@ __device__ __forceinline__ unsigned open_groups(const TopkArgs& A, const R (&v)[
     b2 = b2 < o2 ? o2 : b2;
     b2 = b2 < lo ? lo : b2;
   }
-  const R val = b1 + (A.group_top == 2 && b2 > (R)-inf ? b2 : R(0));
+  const R val = group_value(b1, b2, A.group_top);
   int ahead = 0;
   for (int h = 0; h < A.groups; h++) {
     const R o = __shfl_sync(kFull, val, h * L);
@@ -193,10 +214,10 @@ __device__ __forceinline__ unsigned open_groups(const TopkArgs& A, const R (&v)[
   }
   const bool in = g < A.groups && ahead < A.topk_groups;
   if (sizeof(R) == 4 && margin > 0.f && A.topk_groups < A.groups) {
-    const uint32_t k = key_of((float)val);
-    const float least = value_of(~warp_max(in ? ~k : 0u));
-    const float most = value_of(warp_max(in || g >= A.groups ? kKeyNegInf : k));
-    near = most > -inf && !(least - most > margin + 0x1p-20f * fmaxf(fabsf(least), fabsf(most)));
+    const float slack = group_slack((float)b1, (float)b2, A.group_top);
+    const float least = value_of(~warp_max(in ? ~key_of((float)val - slack) : 0u));
+    const float most = value_of(warp_max(in || g >= A.groups ? kKeyNegInf : key_of((float)val + slack)));
+    near = groups_near(least, most, margin);
   }
   return __ballot_sync(kFull, in);
 }
@@ -219,7 +240,7 @@ __device__ __forceinline__ void close_groups_in_lanes(const TopkArgs& A, const f
   const float inf = topk_inf();
   const int seg = A.seg, per = 32 >> A.seg_log2;  // groups in a chunk of 32 * VEC experts
   const int mine = lane >> A.seg_log2;
-  float val[C];
+  float val[C], slack[C];
   int ahead[C];
 #pragma unroll
   for (int c = 0; c < C; c++) {
@@ -235,7 +256,8 @@ __device__ __forceinline__ void close_groups_in_lanes(const TopkArgs& A, const f
       b2 = fmaxf(fmaxf(b2, o2), fminf(b1, o1));
       b1 = fmaxf(b1, o1);
     }
-    val[c] = b1 + (A.group_top == 2 && b2 > -inf ? b2 : 0.f);
+    val[c] = group_value(b1, b2, A.group_top);
+    slack[c] = group_slack(b1, b2, A.group_top);
     ahead[c] = 0;
   }
 #pragma unroll
@@ -251,14 +273,14 @@ __device__ __forceinline__ void close_groups_in_lanes(const TopkArgs& A, const f
 #pragma unroll
   for (int c = 0; c < C; c++) {
     const bool exists = c * per + mine < A.groups, in = exists && ahead[c] < A.topk_groups;
-    if (in) low = max(low, ~key_of(val[c]));
-    if (exists && !in) high = max(high, key_of(val[c]));
+    if (in) low = max(low, ~key_of(val[c] - slack[c]));
+    if (exists && !in) high = max(high, key_of(val[c] + slack[c]));
 #pragma unroll
     for (int j = 0; j < VEC; j++) key[c * VEC + j] = in ? key[c * VEC + j] : 0u;
   }
   if (margin > 0.f && A.topk_groups < A.groups) {
     const float least = value_of(~warp_max(low)), most = value_of(warp_max(high));
-    near = most > -inf && !(least - most > margin + 0x1p-20f * fmaxf(fabsf(least), fabsf(most)));
+    near = groups_near(least, most, margin);
   }
 }
 

@@ -220,6 +220,36 @@ def test_doubtful_rows_among_ordinary_ones(E, groups, off, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("E,groups,off", [(16, 8, 0), (256, 8, 0), (256, 8, 1), (160, 8, 0)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_group_sums_that_cancel(E, groups, off, score):
+    """Groups whose two best values are large and of opposite sign: the sum's
+    error follows the two, not the little that is left of them."""
+    T, n = 20000, E // groups
+    x = logits(E + off, T, E + 8)[:, off:off + E]
+    for size in (4096.0, 3.0e38):
+        bias = torch.full((E,), -size).cuda()
+        bias[::n] = size
+        kw = dict(score=score, bias=bias, groups=groups, topk_groups=groups // 2, group_top=2)
+        ids, _ = B.iqk_moe_topk(x, 6, **kw)
+        assert torch.equal(ids, choice(x, 6, **kw)), size
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("E,off", [(16, 0), (256, 0), (256, 1)])
+def test_group_sums_past_float32(E, off):
+    """A group whose two best values add up to less than float32's lowest
+    number is still ahead of one that is masked throughout."""
+    T, n = 64, E // 8
+    x = logits(E + off, T, E + 8)[:, off:off + E]
+    bias = torch.full((E,), -3.0e38).cuda()
+    bias[:3 * n] = -math.inf
+    for topk_groups in (2, 5, 6):
+        check(x, 2 * topk_groups, f"open {topk_groups}", score="sigmoid", bias=bias, groups=8, topk_groups=topk_groups,
+              group_top=2)
+
+
+@pytest.mark.gpu
 def test_many_tokens():
     x = logits(11, 65536, 256, torch.bfloat16)
     ids, p = B.iqk_moe_topk(x, 6)
