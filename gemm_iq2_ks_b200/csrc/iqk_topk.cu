@@ -130,13 +130,20 @@ __device__ __forceinline__ Norm<float> quick_norm(const float (&x)[NV], float mo
   for (int i = 0; i < NV; i++) s += x[i] == most ? 1.f : x[i] > -topk_inf() ? __expf(x[i] - most) : 0.f;
   return {most, __fdividef(1.f, warp_sum(s))};
 }
-// exp(-d) by the hardware is within (1.5 d + 5) 2^-24 of itself and d exp(-d)
-// at most 0.37; sum, reciprocal and product add 2^-24 to 2^-23 each. A sigmoid
-// is then within 2^-21; a softmax within (NV + 24) 2^-24 of the largest score,
-// each of the NV + 5 additions of its sum another 2^-24.
+// Bounds of its error, in units u = 2^-24. __expf(y) is documented to be within
+// 2 + 1.173 |y| steps of at most 2 u each; the rounding of y = x - most adds
+// |y| u. So a softmax's exponential at distance d has a relative error of
+// (4 + 3.35 d) u, absolute never above 4 u. In their sum the distances count by
+// weight, sum p_i d_i <= ln n for n terms (the entropy's bound), so with its
+// NV + 5 additions it is within (4 + 3.35 ln(32 NV) + NV + 5) u; reciprocal (2
+// steps) and product add 5 u. With ln(1024) = 6.94 that makes NV + 42, of the
+// largest score. A sigmoid's exponential is within 4 u absolute, 1 + e within
+// 5 u, the quotient within 9 u of itself, the product with e <= 1 within 9 u.
+// Rows in doubt are dear (one whose groups are takes 2048 x 256 from 8 to
+// 14 us), so the bounds are no wider than that.
 template <int NV>
 __device__ __forceinline__ float score_bound(const Norm<float>& n, bool sigmoid) {
-  return sigmoid ? 0x1p-21f : (NV + 24) * 0x1p-24f * fminf(n.total, 1.f);
+  return sigmoid ? 10 * 0x1p-24f : (NV + 44) * 0x1p-24f * fminf(n.total, 1.f);
 }
 
 // Selection value of an expert with logit x and bias b; -inf where it is masked.
@@ -152,9 +159,9 @@ __device__ __forceinline__ float value_of_expert(const Norm<float>& n, bool sigm
 // A group's value from its best two selection values, and what float32
 // arithmetic may have moved it by, beyond the scores' own error: half a step
 // for each of the two (score + bias) and for their sum, each relative to a
-// number of at most the larger one's size, twice; so 2^-22 of that size, and
-// as much again for the comparison's own roundings. The sum itself may be far
-// smaller than the two. A sum below float32's range stays ahead of -inf.
+// number of at most the larger one's size m, twice: 4 m 2^-24; the rounding of
+// value +- slack adds 2 m 2^-24. The sum itself may be far smaller than the
+// two. A sum below float32's range stays ahead of -inf.
 template <typename R>
 __device__ __forceinline__ R group_value(R b1, R b2, int group_top) {
   const R v = b1 + (group_top == 2 && b2 > (R)-topk_inf() ? b2 : R(0));
@@ -162,7 +169,7 @@ __device__ __forceinline__ R group_value(R b1, R b2, int group_top) {
 }
 __device__ __forceinline__ float group_slack(float b1, float b2, int group_top) {
   const float m = fmaxf(fabsf(b1), group_top == 2 && b2 > -topk_inf() ? fabsf(b2) : 0.f);
-  return 0x1p-21f * fminf(m, 3.402823466e38f);
+  return 6 * 0x1p-24f * fminf(m, 3.402823466e38f);
 }
 // Whether the last open group (lowest value `least`, less its slack) may not be
 // ahead of the first closed one (`most`, its slack added).

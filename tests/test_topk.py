@@ -164,6 +164,24 @@ def test_near_ties_follow_float64(score):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E", [32, 256, 1024])
+@pytest.mark.parametrize("spread", [1.0, 6.0])
+def test_near_ties_of_far_logits(score, E, spread):
+    """As above with logits far apart, where the hardware exponential's error is
+    largest: selection values that differ by 2^-24 of the largest score to 2^-18."""
+    T = 512
+    g = torch.Generator().manual_seed(E)
+    x = spread * torch.randn((1, E), generator=g)
+    s = torch.softmax(x[0].double(), -1) if score == "softmax" else torch.sigmoid(x[0].double())
+    top = float(s.max())
+    bias = (top - s + top * torch.exp2(torch.randint(-24, -17, (E,), generator=g).double())).float()
+    x = (x * (1 + 2.0 ** -22 * torch.randint(-4, 5, (T, 1), generator=g))).cuda()
+    check(x, 16, "far", score=score, bias=bias.cuda())
+    check(x, 6, "far, groups", score=score, bias=bias.cuda(), groups=8, topk_groups=3, group_top=2)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_strides_outputs_and_streams(dtype):
     """Rows inside a wider matrix at any offset, on another stream, into given
