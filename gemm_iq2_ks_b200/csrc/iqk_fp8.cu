@@ -147,6 +147,23 @@ __device__ __forceinline__ float4 ld_peer4(uint32_t addr) {
   return v;
 }
 
+// The two scales of a block's sum as factors, of which `big` is applied first
+// and `small` in the multiply-add: 1 and their product where that is a normal
+// number. Where it would overflow or lose bits (the sum times it may
+// well be an ordinary number) the larger scale and the smaller one: block sums
+// are 0 or between 2^-18 and 2^25, so no product on the way is out of range
+// unless the result is.
+struct Scale {
+  float big, small;
+};
+__device__ __forceinline__ bool not_normal(float p) { return (((__float_as_uint(p) >> 23) + 1) & 255u) <= 1u; }
+__device__ __forceinline__ Scale scale_of(float a, float b) {
+  const float p = a * b;
+  const bool far = not_normal(p) && a != 0.f && b != 0.f && fabsf(a) <= 3.402823466e38f && fabsf(b) <= 3.402823466e38f;
+  const bool first = fabsf(a) >= fabsf(b);
+  return {far ? (first ? a : b) : 1.f, far ? (first ? b : a) : p};
+}
+
 // Output element of the plain product.
 __device__ __forceinline__ void put_y(const Fp8Args& A, int64_t i, float v) {
   if (A.f32) {
@@ -201,9 +218,10 @@ constexpr int kPitch(int BN) { return BN + 4; }  // floats between rows of the s
 constexpr int kStageOut = 2048;                  // bytes of one warp's store staging: 32 rows x 16 floats
 constexpr int kStaging(bool gu) { return gu ? 4 * kBM * 4 : kEpiWarps * kStageOut; }
 // With the scales of a step beside each accumulator: [2 weight blocks][128 rows]
-// products of token and block scale, written by two warps of their own.
+// products of token and block scale (or the smaller of the two, and the larger
+// one in a second table, see scale_of), written by two warps of their own.
 constexpr size_t kGemmSmem(int BN, bool gu, bool pair) {
-  return kGemmRing(BN, pair) + kStaging(gu) + 512 / BN * 2 * kBM * 4 + 256 + 1024;
+  return kGemmRing(BN, pair) + kStaging(gu) + 2 * (512 / BN * 2 * kBM * 4) + 256 + 1024;
 }
 static_assert(kBM * kPitch(256) * 4 <= kGemmRing(256, false) && kBM * kPitch(128) * 4 <= kGemmRing(128, false),
               "accumulators");
@@ -327,31 +345,63 @@ __device__ __forceinline__ void tmem_wait_ld16(uint32_t (&r)[16]) {
                : "memory");
 }
 
+// The warp's lanes of N columns times big(column), in tensor memory: for the few
+// steps of few-token products whose scales are not applied as one factor
+// (scale_of). It stands ahead of the ordinary path, whose registers stay as
+// they are.
+template <int N, typename F>
+__device__ __forceinline__ void scale_tmem(uint32_t taddr, F big) {
+#pragma unroll 1
+  for (int c0 = 0; c0 < N; c0 += 8) {
+    float v[8];
+    tmem_ld8(taddr + c0, v);
+#pragma unroll
+    for (int c = 0; c < 8; c++) v[c] *= big(c0 + c);
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr + c0),
+                 "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                 : "memory");
+  }
+  tmem_wait_st();
+}
+
 // Two float32 fused multiply-adds in one instruction: acc += (lo, hi) * (s, s).
 __device__ __forceinline__ void fma2(uint64_t& acc, uint32_t lo, uint32_t hi, uint64_t s) {
   asm("{\n\t.reg .b64 v;\n\tmov.b64 v, {%1, %2};\n\tfma.rn.f32x2 %0, v, %3, %0;\n\t}"
       : "+l"(acc)
       : "r"(lo), "r"(hi), "l"(s));
 }
-__device__ __forceinline__ uint64_t twice(float s) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(s));
-  return r;
-}
 __device__ __forceinline__ float lo_of(uint64_t v) { return __uint_as_float((uint32_t)v); }
 __device__ __forceinline__ float hi_of(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
 
 // The same for 32 columns straight from tensor memory, as one block: the loaded
 // registers stay in it, paired where they are (the separate forms copy them
-// first). One register too many for the gate_up kernels, which spill with it.
-#define IQK_FMA2(lo, hi, a) "mov.b64 p, {t" lo ", t" hi "};\n\tfma.rn.f32x2 %" a ", p, %17, %" a ";\n\t"
-__device__ __forceinline__ void ld_fma32(uint32_t taddr, uint64_t* a, uint64_t s) {
+// first).
+// `sc`: shared-memory address of the row's factor `small`, `big` BIG bytes
+// behind it (scale_of); both are on their way while the sums are.
+#define IQK_FMA2(lo, hi, a) "mov.b64 p, {t" lo ", t" hi "};\n\tfma.rn.f32x2 %" a ", p, s, %" a ";\n\t"
+#define IQK_MUL(i) "mul.rn.f32 t" i ", t" i ", g;\n\t"
+template <int BIG>
+__device__ __forceinline__ void ld_fma32(uint32_t taddr, uint64_t* a, uint32_t sc) {
   asm volatile(
-      "{\n\t.reg .b32 t<32>;\n\t.reg .b64 p;\n\t"
+      "{\n\t.reg .b32 t<32>;\n\t.reg .b64 p, s;\n\t.reg .f32 f, g;\n\t.reg .pred q;\n\t"
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {t0, t1, t2, t3, t4, t5, t6, t7, t8, t9, t10, t11, "
       "t12, t13, t14, t15, t16, t17, t18, t19, t20, t21, t22, t23, "
       "t24, t25, t26, t27, t28, t29, t30, t31}, [%16];\n\t"
+      "ld.shared.f32 f, [%17];\n\tld.shared.f32 g, [%17+%18];\n\t"
+      "mov.b64 s, {f, f};\n\t"
+      "setp.neu.f32 q, g, 0f3f800000;\n\t"
+      "vote.sync.any.pred q, q, 0xffffffff;\n\t"
       "tcgen05.wait::ld.sync.aligned;\n\t"
+      "@!q bra.uni ONE_%=;\n\t"
+      IQK_MUL("0") IQK_MUL("1") IQK_MUL("2") IQK_MUL("3")
+      IQK_MUL("4") IQK_MUL("5") IQK_MUL("6") IQK_MUL("7")
+      IQK_MUL("8") IQK_MUL("9") IQK_MUL("10") IQK_MUL("11")
+      IQK_MUL("12") IQK_MUL("13") IQK_MUL("14") IQK_MUL("15")
+      IQK_MUL("16") IQK_MUL("17") IQK_MUL("18") IQK_MUL("19")
+      IQK_MUL("20") IQK_MUL("21") IQK_MUL("22") IQK_MUL("23")
+      IQK_MUL("24") IQK_MUL("25") IQK_MUL("26") IQK_MUL("27")
+      IQK_MUL("28") IQK_MUL("29") IQK_MUL("30") IQK_MUL("31")
+      "ONE_%=:\n\t"
       IQK_FMA2("0", "1", "0")
       IQK_FMA2("2", "3", "1")
       IQK_FMA2("4", "5", "2")
@@ -371,8 +421,9 @@ __device__ __forceinline__ void ld_fma32(uint32_t taddr, uint64_t* a, uint64_t s
       "}"
       : "+l"(a[0]), "+l"(a[1]), "+l"(a[2]), "+l"(a[3]), "+l"(a[4]), "+l"(a[5]), "+l"(a[6]), "+l"(a[7]),
         "+l"(a[8]), "+l"(a[9]), "+l"(a[10]), "+l"(a[11]), "+l"(a[12]), "+l"(a[13]), "+l"(a[14]), "+l"(a[15])
-      : "r"(taddr), "l"(s));
+      : "r"(taddr), "r"(sc), "n"(BIG));
 }
+#undef IQK_MUL
 #undef IQK_FMA2
 
 // Instruction descriptor, kind::f8f6f4: e4m3 A and B (format code 0), float32
@@ -514,7 +565,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   uint8_t* staging = smem + kGemmRing(BN, PAIR);
   float* scales = reinterpret_cast<float*>(staging + kStaging(GU));
-  uint64_t* full = reinterpret_cast<uint64_t*>(scales + NBUF * 2 * kBM);
+  constexpr int kBigs = NBUF * 2 * kBM;  // behind the table of the smaller factors: that of the larger ones
+  uint64_t* full = reinterpret_cast<uint64_t*>(scales + 2 * kBigs);
   uint64_t* empty = full + ST;
   uint64_t* tfull = empty + ST;
   uint64_t* tfree = tfull + NBUF;
@@ -643,6 +695,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     if (warp >= kScaleWarp) {
       // rows 64 w + lane and 32 on, one step's scales fetched ahead
       const int r = 64 * (warp - kScaleWarp) + lane;
+      uint32_t dirty = ~0u;  // accumulators whose table of larger factors is not all 1
       int it = 0;
       bool ok = true;
       for (int tile = first; tile < tiles && ok; tile += step) {
@@ -662,11 +715,28 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           if (!(ok = gemm_wait(&(PAIR ? sfree : tfree)[it % NBUF], ((it / NBUF) & 1) ^ 1, abort_flag, A.wait_ns)))
             break;
           float* dst = scales + (it % NBUF) * 2 * kBM + r;
-          dst[0] = a0 * b0;
-          dst[32] = a1 * b0;
-          if (BN == 256) {
-            dst[kBM] = a0 * b1;
-            dst[kBM + 32] = a1 * b1;
+          bool far = false;
+          auto each = [&](auto f) {
+            f(0, a0, b0);
+            f(32, a1, b0);
+            if (BN == 256) {
+              f(kBM, a0, b1);
+              f(kBM + 32, a1, b1);
+            }
+          };
+          each([&](int i, float a, float b) {
+            dst[i] = a * b;
+            far |= not_normal(a * b);
+          });
+          if (__any_sync(0xffffffffu, far) || (dirty >> (it % NBUF) & 1)) {
+            far = false;
+            each([&](int i, float a, float b) {
+              const Scale f = scale_of(a, b);
+              dst[i] = f.small;
+              dst[kBigs + i] = f.big;
+              far |= f.big != 1.f;
+            });
+            dirty = (dirty & ~(1u << it % NBUF)) | (uint32_t)(__any_sync(0xffffffffu, far) != 0) << it % NBUF;
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&tfull[it % NBUF]);
@@ -720,22 +790,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         const int b = it % NBUF;
         if (!(ok = ok && gemm_wait(&tfull[b], (it / NBUF) & 1, abort_flag, A.wait_ns))) continue;
         tc_fence_after();
-        const float* sc = scales + b * 2 * kBM + 32 * q + lane;
-        const uint64_t sw = twice(sc[BN == 256 && !GU && part >= 2 ? kBM : 0]), su = GU ? twice(sc[kBM]) : sw;
+        const float* sc = scales + b * 2 * kBM + (BN == 256 && !GU && part >= 2 ? kBM : 0) + 32 * q + lane;
         if (rows_in) {
           const uint32_t col = lanes + b * BN + (GU ? part * 32 : part * NC);
 #pragma unroll
-          for (int c0 = 0; c0 < NC; c0 += 32) {
-            if constexpr (GU) {
-              uint32_t r[32];
-              tmem_ld32(col + (c0 ? 128 : 0), r);
-              tmem_wait_ld(r);
-#pragma unroll
-              for (int c = 0; c < 16; c++) fma2(acc[c0 / 2 + c], r[2 * c], r[2 * c + 1], c0 ? su : sw);
-            } else {
-              ld_fma32(col + c0, acc + c0 / 2, sw);
-            }
-          }
+          for (int c0 = 0; c0 < NC; c0 += 32)
+            ld_fma32<kBigs * 4>(col + (GU && c0 ? 128 : c0), acc + c0 / 2, smem_u32(sc) + (GU && c0 ? kBM * 4 : 0));
         }
         tc_fence_before();
         __syncwarp();
@@ -879,7 +939,7 @@ constexpr int kSkStage(bool gu, int TN) { return ((gu ? 256 : 128) + TN) * kFp8B
 constexpr int kSkStages(bool gu) { return gu ? 3 : 5; }
 constexpr int kSkBufs = 4;  // accumulators in tensor memory: at most 256 columns for each of two CTAs
 constexpr int kSkRing(bool gu, int TN) { return kSkStages(gu) * kSkStage(gu, TN); }
-constexpr size_t kSkSmem(bool gu, int TN) { return kSkRing(gu, TN) + 4 * 2 * kSkinnyMaxT * 4 + 256 + 1024; }
+constexpr size_t kSkSmem(bool gu, int TN) { return kSkRing(gu, TN) + 2 * (4 * 2 * kSkinnyMaxT * 4) + 256 + 1024; }
 static_assert(kSkRing(true, 32) >= 32 * 256 * 4 && kSkRing(false, 32) >= 32 * 128 * 4, "accumulators");
 static_assert(kSkSmem(true, 32) <= 113 * 1024 && kSkSmem(false, 32) <= 113 * 1024, "two CTAs on an SM");
 
@@ -892,7 +952,8 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   float* table = reinterpret_cast<float*>(smem + kSkRing(GU, TN));  // [4 warps][2][32]
-  uint64_t* full = reinterpret_cast<uint64_t*>(table + 4 * 2 * kSkinnyMaxT);
+  constexpr int kBigs = 4 * 2 * kSkinnyMaxT;  // a second one behind it, for the larger scales (scale_of)
+  uint64_t* full = reinterpret_cast<uint64_t*>(table + 2 * kBigs);
   uint64_t* empty = full + ST;
   uint64_t* tfull = empty + ST;
   uint64_t* tfree = tfull + NBUF;
@@ -991,9 +1052,20 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
     if (A.expire && warp == 0) ok = gemm_wait(never, 0, abort_flag, A.wait_ns);  // testing hook: this wait runs out
     for (int i = 0; ok && i < steps; i++) {
       const int b = i % NBUF;
-      __syncwarp();
       tab[lane] = xn * wn;
       if (GU) tab[kSkinnyMaxT + lane] = xn * un;
+      bool far = __any_sync(0xffffffffu, not_normal(xn * wn) || (GU && not_normal(xn * un)));
+      if (far) {
+        far = false;
+#pragma unroll
+        for (int m = 0; m < M; m++) {
+          const Scale f = scale_of(xn, m ? un : wn);
+          tab[m * kSkinnyMaxT + lane] = f.small;
+          tab[kBigs + m * kSkinnyMaxT + lane] = f.big;
+          far |= f.big != 1.f;
+        }
+        far = __any_sync(0xffffffffu, far);
+      }
       if (i + 1 < steps) {
         xn = xs[i + 1];
         wn = ws[i + 1];
@@ -1002,6 +1074,10 @@ __global__ void __launch_bounds__(kSkinnyThreads, 2)
       __syncwarp();
       if (!(ok = gemm_wait(&tfull[b], (i / NBUF) & 1, abort_flag, A.wait_ns))) break;
       tc_fence_after();
+      if (far)
+#pragma unroll
+        for (int m = 0; m < M; m++)
+          scale_tmem<TN>(lanes + (b * M + m) * TN, [&](int c) { return tab[kBigs + m * kSkinnyMaxT + c]; });
 #pragma unroll
       for (int m = 0; m < M; m++)
 #pragma unroll

@@ -532,8 +532,12 @@ int iqk_fp8_quantize(const uint16_t* x, int64_t row_stride, int32_t T, int32_t c
  *   add: NULL, or device [T][rows] of y's type; may be y itself
  *   y: device bf16 or float32 (y_dtype) [T][rows], written completely
  * rows >= 1, cols a positive multiple of 16, T <= 65536, rows <= 2^30, fewer
- * than 2^31 scales in each operand; wq and xq 16-byte aligned. float32 accumulation, one rounding to y's type; the order of the
- * sums depends on the sizes only, so equal calls give equal results.
+ * than 2^31 scales in each operand; wq and xq 16-byte aligned; y overlaps no
+ * input but add. float32 accumulation, one rounding to y's type; the order of
+ * the sums depends on the sizes only, so equal calls give equal results. The
+ * scales are any float32 numbers: xs ws itself may lie outside float32's range
+ * as long as the terms of the sum over b and their partial sums do not (such a
+ * block takes somewhat longer).
  */
 int iqk_fp8_linear(const uint8_t* wq, const float* ws, int32_t rows, int32_t cols, const uint8_t* xq, const float* xs,
                    int32_t T, const void* add, void* y, int32_t y_dtype, void* stream);

@@ -220,6 +220,78 @@ def test_linear_outputs_at_any_element(T, dtype):
     assert buf[0] == -5 and (buf[-2:] == -5).all()
 
 
+def far_operands(T, rows, cols, weights=1):
+    """Operands whose scales' products leave float32's normal numbers although
+    the results do not. Even tokens: 2^130 and more (in every third block),
+    under the smallest codes of both operands in one column of the block and
+    zeros; odd ones: 2^-142 to 2^-133 (in the block behind), under ordinary
+    codes, and scales of 0. Returns xq, xs and (codes, scales) of each weight
+    matrix; the scales of the second are ordinary where the first's are not."""
+    nkb = blocks(cols)
+    kind = torch.arange(nkb) % 3
+    xq, xs = operand(1, T, cols, 1)
+    x = xq.view(torch.uint8)
+    x[::2] &= 0x80         # signed zeros ...
+    x[::2, ::128] |= 1     # ... and 2^-9
+    r = (1 + torch.rand((T, nkb), generator=gen(2))).cuda()
+    xs[::2] = torch.where((kind == 0).cuda(), r[::2] * 2.0 ** 70, torch.zeros(()).cuda())
+    xs[1::2] = torch.where((kind == 1).cuda(), r[1::2] * torch.exp2(torch.linspace(-82, -74, nkb)).cuda(), torch.zeros(()).cuda())
+    out = []
+    for n in range(weights):
+        wq, ws = operand(3 + 2 * n, rows, cols, 128)
+        w = wq.view(torch.uint8)
+        w[:, ::128] &= 0x83    # at most 3 * 2^-9
+        r = (1 + torch.rand(ws.shape, generator=gen(8 + n))).cuda()
+        far = [(60.0, -60.0), (-60.0, 100.0)][n]
+        ws = torch.where((kind == 0).cuda(), r * 2.0 ** far[0], torch.where((kind == 1).cuda(), r * 2.0 ** far[1], ws))
+        out.append((wq, ws))
+    return (xq, xs, *out)
+
+
+FAR_SIZES = [(1, 144, 512), (5, 528, 4096), (24, 144, 400), (40, 528, 2064), (300, 1008, 400), (700, 2064, 272),
+             (2600, 1104, 400), (5200, 2096, 256)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,rows,cols", FAR_SIZES)
+def test_linear_scales_of_any_size(T, rows, cols):
+    """Only the result has to be in float32's range. Two roundings for a block
+    instead of one (its sum times one scale, then times the other) are within
+    the 8 that the bound counts; 2^-148 for each block is what is lost below
+    float32's normal numbers."""
+    xq, xs, (wq, ws) = far_operands(T, rows, cols)
+    y = B.iqk_fp8_linear(wq, ws, xq, xs, dtype=torch.float32)
+    ref, S, tol = product(wq, ws, xq, xs)
+    assert 2.0 ** 100 < S[::2].max() < 2.0 ** 127 and (T == 1 or 2.0 ** -126 < S[1::2].max() < 2.0 ** -100)
+    err = (y.double() - ref).abs()
+    assert (err <= tol * (1 + 2.0 ** -24) + 2.0 ** -24 * ref.abs() + 2.0 ** -148 * blocks(cols)).all()
+    xq.view(torch.uint8)[0] = 0  # a token of zeros under the largest scales
+    assert (B.iqk_fp8_linear(wq, ws, xq, xs, dtype=torch.float32)[0] == 0).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,rows,cols", FAR_SIZES)
+def test_gate_up_scales_of_any_size(T, rows, cols):
+    """As check_h, with either matrix's products out of range."""
+    xq, xs, *w = far_operands(T, rows, cols, 2)
+    for (gq, gs), (uq, us) in (w, w[::-1]):
+        q, s = B.iqk_fp8_gate_up(gq, gs, uq, us, xq, xs)
+        g, _, dg = product(gq, gs, xq, xs)
+        u, _, du = product(uq, us, xq, xs)
+        dg, du = dg + 2.0 ** -148 * blocks(cols), du + 2.0 ** -148 * blocks(cols)
+        silu = g * torch.sigmoid(g)
+        h = silu * u
+        dh = 1.1 * dg * (u.abs() + du) + silu.abs() * du + 2.0 ** -20 * h.abs() + 2.0 ** -148
+        for b in range(blocks(rows)):
+            c = slice(b * 128, min((b + 1) * 128, rows))
+            m, dm = h[:, c].abs().amax(1), dh[:, c].amax(1)
+            assert (m > 2.0 ** -100).all()
+            assert ((s[:, b].double() - m / 448).abs() <= dm / 448 + 2.0 ** -22 * m / 448).all()
+            sb = s[:, b].double()[:, None]
+            bound = (2.0 ** -4 * (h[:, c].abs() + dh[:, c]) + 2.0 ** -10 * sb + dh[:, c]) * (1 + 2.0 ** -20)
+            assert ((q[:, c].double() * sb - h[:, c]).abs() <= bound).all()
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("T", [2, 150])
 def test_linear_nan_stays_in_its_row(T):
