@@ -625,7 +625,7 @@ __global__ void __launch_bounds__(kTopkWarps * 32, NV <= 8 ? 4 : NV == 16 ? 2 : 
 template <int NV>
 int launch_nv(const TopkArgs& a, int vec, bool bf16, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((a.T + kTopkWarps - 1) / kTopkWarps));
+  cfg.gridDim = dim3((unsigned)(((int64_t)a.T + kTopkWarps - 1) / kTopkWarps));
   cfg.blockDim = dim3(kTopkWarps * 32);
   cfg.dynamicSmemBytes = a.groups > 1 ? (size_t)kTopkWarps * a.smem_row * sizeof(double) : 0;
   cfg.stream = st;

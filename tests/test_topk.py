@@ -287,6 +287,17 @@ def test_rows_past_32_bit_offsets():
     check(x, 6, "far rows")
 
 
+@pytest.mark.gpu
+def test_as_many_rows_as_an_int_counts():
+    """T = 2^31 - 1 rows of one expert: the last block is rounded up past it."""
+    T = 2 ** 31 - 1
+    x = torch.zeros((T, 1), dtype=torch.bfloat16, device="cuda")
+    ids = torch.full((T, 1), -1, dtype=torch.int32, device="cuda")
+    _, p = B.iqk_moe_topk(x, 1, ids=ids)
+    assert int(ids.amin()) == int(ids.amax()) == 0
+    assert float(p.amin()) == float(p.amax()) == 1.0
+
+
 def test_refusals_on_the_host():
     L = B.lib()
 
