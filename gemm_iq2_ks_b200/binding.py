@@ -206,8 +206,20 @@ class Weights:
                    if t is not None)
 
 
-def _empty(shape, dtype, device):
-    return _torch().empty(shape, dtype=dtype, device=device)
+def _empty(shape, dtype, device, stream=None):
+    """Memory for a call on `stream` (None: the current one), from that stream's
+    pool: a block of another stream's pool may still be in use there, or be
+    given away there while the call runs. It is recorded for the current stream
+    too, where the caller may read it."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    here = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if here != stream:
+        t.record_stream(here)
+    return t
 
 
 # ------------------------------------------------------------------ entry points
@@ -220,7 +232,7 @@ def iqk_prefill_a_tile(w: Weights, expert: int, row0: int, nrows: int, values, o
     """The prefill producer's bf16 A operand of rows [row0, row0 + nrows) of
     one expert, in k order ([nrows, cols] bf16)."""
     torch = _torch()
-    out = _empty((nrows, w.cols), torch.bfloat16, w.qs.device) if out is None else out
+    out = _empty((nrows, w.cols), torch.bfloat16, w.qs.device, stream) if out is None else out
     v = _values(values)
     _check(lib().iqk_prefill_a_tile(ctypes.byref(w.c), expert, row0, nrows, v.ctypes.data, out.data_ptr(),
                                     _stream(stream)), "iqk_prefill_a_tile")
@@ -229,7 +241,7 @@ def iqk_prefill_a_tile(w: Weights, expert: int, row0: int, nrows: int, values, o
 
 def iqk_dequant(w: Weights, expert: int, values, out=None, stream=None):
     torch = _torch()
-    out = _empty((w.rows, w.cols), torch.float32, w.qs.device) if out is None else out
+    out = _empty((w.rows, w.cols), torch.float32, w.qs.device, stream) if out is None else out
     v = _values(values)
     _check(lib().iqk_dequant(ctypes.byref(w.c), expert, v.ctypes.data, out.data_ptr(), _stream(stream)),
            "iqk_dequant")
@@ -238,7 +250,7 @@ def iqk_dequant(w: Weights, expert: int, values, out=None, stream=None):
 
 def iqk_dequant_bf16(w: Weights, expert: int, values, out=None, stream=None):
     torch = _torch()
-    out = _empty((w.rows, w.cols), torch.bfloat16, w.qs.device) if out is None else out
+    out = _empty((w.rows, w.cols), torch.bfloat16, w.qs.device, stream) if out is None else out
     v = _values(values)
     _check(lib().iqk_dequant_bf16(ctypes.byref(w.c), expert, v.ctypes.data, out.data_ptr(), _stream(stream)),
            "iqk_dequant_bf16")
@@ -249,7 +261,7 @@ def iqk_dequant_floor(w: Weights, expert: int, bf16: bool = False, out=None, str
     """The dequantizer's deleted-decode floor: int32 [rows][cols] (or
     [rows][cols/2] with bf16), the integer signature of every loaded word."""
     torch = _torch()
-    out = _empty((w.rows, w.cols // 2 if bf16 else w.cols), torch.int32, w.qs.device) if out is None else out
+    out = _empty((w.rows, w.cols // 2 if bf16 else w.cols), torch.int32, w.qs.device, stream) if out is None else out
     _check(lib().iqk_dequant_floor(ctypes.byref(w.c), expert, int(bool(bf16)), out.data_ptr(), _stream(stream)),
            "iqk_dequant_floor")
     return out
@@ -259,17 +271,17 @@ def iqk_gemv_workspace_bytes(T: int, rows: int, cols: int) -> int:
     return lib().iqk_gemv_workspace_bytes(T, rows, cols)
 
 
-def workspace(nbytes: int, device="cuda"):
-    """A 256-byte aligned device workspace (torch allocations are)."""
-    return _empty((max(nbytes, 256),), _torch().uint8, device)
+def workspace(nbytes: int, device="cuda", stream=None):
+    """A 256-byte aligned device workspace (torch allocations are), for calls on `stream`."""
+    return _empty((max(nbytes, 256),), _torch().uint8, device, stream)
 
 
 def iqk_gemv(w: Weights, expert: int, values, x, y=None, ws=None, stream=None):
     torch = _torch()
     T = x.shape[0]
-    y = _empty((T, w.rows), torch.float32, x.device) if y is None else y
+    y = _empty((T, w.rows), torch.float32, x.device, stream) if y is None else y
     need = iqk_gemv_workspace_bytes(T, w.rows, w.cols)
-    ws = workspace(need, x.device) if ws is None else ws
+    ws = workspace(need, x.device, stream) if ws is None else ws
     v = _values(values)
     _check(lib().iqk_gemv(ctypes.byref(w.c), expert, v.ctypes.data, x.data_ptr(), T, y.data_ptr(), ws.data_ptr(),
                           ws.numel(), _stream(stream)), "iqk_gemv")
@@ -280,7 +292,7 @@ def iqk_gemv_static(w: Weights, expert: int, values, x, y=None, stream=None):
     """iqk_gemv with the library's static scratch (no workspace argument)."""
     torch = _torch()
     T = x.shape[0]
-    y = _empty((T, w.rows), torch.float32, x.device) if y is None else y
+    y = _empty((T, w.rows), torch.float32, x.device, stream) if y is None else y
     v = _values(values)
     _check(lib().iqk_gemv_static(ctypes.byref(w.c), expert, v.ctypes.data, x.data_ptr(), T, y.data_ptr(),
                                  _stream(stream)), "iqk_gemv_static")
@@ -295,12 +307,12 @@ def iqk_switch_linear(w: Weights, values, x, ids, mode: int = 0, y=None, ws=None
     """y[t, j] = W_{ids[t, j]} x[t] (float32 [T, topk, rows])."""
     torch = _torch()
     T, topk = ids.shape
-    y = _empty((T, topk, w.rows), torch.float32, x.device) if y is None else y
+    y = _empty((T, topk, w.rows), torch.float32, x.device, stream) if y is None else y
     if ws is None:
         need = iqk_switch_linear_workspace_bytes(mode, T, topk, w.experts, w.rows, w.cols)
         if need == 0:
             raise RuntimeError("iqk_switch_linear: the mode cannot take this shape")
-        ws = workspace(need, x.device)
+        ws = workspace(need, x.device, stream)
     v = _values(values)
     _check(lib().iqk_switch_linear(ctypes.byref(w.c), v.ctypes.data, x.data_ptr(), T, ids.data_ptr(), topk,
                                    y.data_ptr(), mode, ws.data_ptr(), ws.numel(), _stream(stream)),
@@ -322,11 +334,11 @@ def iqk_moe_workspace_layout(mode: int, T: int, topk: int, experts: int, hidden:
 def _moe(fn, mode, gate, up, down, values, x, ids, p, y, ws, stream):
     torch = _torch()
     T, topk = ids.shape
-    y = _empty((T, down.rows), torch.bfloat16, x.device) if y is None else y
+    y = _empty((T, down.rows), torch.bfloat16, x.device, stream) if y is None else y
     need = iqk_moe_workspace_bytes(mode, T, topk, gate.experts, gate.cols, gate.rows)
     if need == 0:
         raise ValueError("unsupported token count / topk for this call")
-    ws = workspace(need, x.device) if ws is None else ws
+    ws = workspace(need, x.device, stream) if ws is None else ws
     v = _values(values)
     _check(fn(ctypes.byref(gate.c), ctypes.byref(up.c), ctypes.byref(down.c), v.ctypes.data, x.data_ptr(), T,
               ids.data_ptr(), p.data_ptr(), topk, y.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream)),
@@ -349,7 +361,7 @@ def iqk_moe_decode_host(gate: Weights, up: Weights, down: Weights, values, x, id
         y = torch.empty((T, down.rows), dtype=torch.bfloat16, pin_memory=True)
     if ws is None:
         ws = workspace(iqk_moe_workspace_bytes(0, T, topk, gate.experts, gate.cols, gate.rows),
-                       torch.device("cuda", torch.cuda.current_device()))
+                       torch.device("cuda", torch.cuda.current_device()), stream)
     v = _values(values)
     _check(lib().iqk_moe_decode_host(ctypes.byref(gate.c), ctypes.byref(up.c), ctypes.byref(down.c), v.ctypes.data,
                                      x.data_ptr(), T, ids.data_ptr(), p.data_ptr(), topk, y.data_ptr(),
@@ -368,9 +380,9 @@ def iqk_moe_decode_shard(gate: Weights, up: Weights, down: Weights, values, x, i
     [expert_base, expert_base + gate.experts); other ids skipped)."""
     torch = _torch()
     T, topk = ids.shape
-    y = _empty((T, down.rows), torch.float32, x.device) if y is None else y
+    y = _empty((T, down.rows), torch.float32, x.device, stream) if y is None else y
     if ws is None:
-        ws = workspace(iqk_moe_workspace_bytes(0, T, topk, gate.experts, gate.cols, gate.rows), x.device)
+        ws = workspace(iqk_moe_workspace_bytes(0, T, topk, gate.experts, gate.cols, gate.rows), x.device, stream)
     v = _values(values)
     _check(lib().iqk_moe_decode_shard(ctypes.byref(gate.c), ctypes.byref(up.c), ctypes.byref(down.c), v.ctypes.data,
                                       x.data_ptr(), T, ids.data_ptr(), p.data_ptr(), topk, expert_base,
@@ -384,9 +396,9 @@ def iqk_moe_prefill_shard(gate: Weights, up: Weights, down: Weights, values, x, 
     """One expert-parallel rank's float32 prefill partial [T, hidden]."""
     torch = _torch()
     T, topk = ids.shape
-    y = _empty((T, down.rows), torch.float32, x.device) if y is None else y
+    y = _empty((T, down.rows), torch.float32, x.device, stream) if y is None else y
     if ws is None:
-        ws = workspace(iqk_moe_workspace_bytes(1, T, topk, gate.experts, gate.cols, gate.rows), x.device)
+        ws = workspace(iqk_moe_workspace_bytes(1, T, topk, gate.experts, gate.cols, gate.rows), x.device, stream)
     v = _values(values)
     _check(lib().iqk_moe_prefill_shard(ctypes.byref(gate.c), ctypes.byref(up.c), ctypes.byref(down.c),
                                        v.ctypes.data, x.data_ptr(), T, ids.data_ptr(), p.data_ptr(), topk,
@@ -400,7 +412,7 @@ def iqk_moe_combine(rows, p, y=None, stream=None):
     torch = _torch()
     T, topk = p.shape
     H = rows.shape[-1]
-    y = _empty((T, H), torch.bfloat16, rows.device) if y is None else y
+    y = _empty((T, H), torch.bfloat16, rows.device, stream) if y is None else y
     _check(lib().iqk_moe_combine(rows.data_ptr(), p.data_ptr(), T, topk, H, y.data_ptr(), _stream(stream)),
            "iqk_moe_combine")
     return y
@@ -408,7 +420,7 @@ def iqk_moe_combine(rows, p, y=None, stream=None):
 
 def iqk_f32_to_bf16(x, out=None, stream=None):
     torch = _torch()
-    out = _empty(tuple(x.shape), torch.bfloat16, x.device) if out is None else out
+    out = _empty(tuple(x.shape), torch.bfloat16, x.device, stream) if out is None else out
     _check(lib().iqk_f32_to_bf16(x.data_ptr(), out.data_ptr(), x.numel(), _stream(stream)), "iqk_f32_to_bf16")
     return out
 
@@ -425,10 +437,11 @@ def iqk_moe_route(ids, experts: int, ws=None, stream=None):
     torch = _torch()
     T, topk = ids.shape
     dev = ids.device
-    counts = _empty((experts,), torch.int32, dev)
-    offsets = _empty((experts + 1,), torch.int32, dev)
-    perm = torch.full((T * topk,), -1, dtype=torch.int32, device=dev)
-    ws = workspace(iqk_route_workspace_bytes(T, topk, experts), dev) if ws is None else ws
+    counts = _empty((experts,), torch.int32, dev, stream)
+    offsets = _empty((experts + 1,), torch.int32, dev, stream)
+    with torch.cuda.stream(stream):  # None: as it is
+        perm = torch.full((T * topk,), -1, dtype=torch.int32, device=dev)
+    ws = workspace(iqk_route_workspace_bytes(T, topk, experts), dev, stream) if ws is None else ws
     _check(lib().iqk_moe_route(ids.data_ptr(), T, topk, experts, counts.data_ptr(), offsets.data_ptr(),
                                perm.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream)), "iqk_moe_route")
     return counts, offsets, perm, ws
@@ -437,7 +450,7 @@ def iqk_moe_route(ids, experts: int, ws=None, stream=None):
 def iqk_floor(w: Weights, expert_list, out=None, stream=None):
     torch = _torch()
     n = expert_list.numel()
-    out = _empty((n, w.rows), torch.int32, expert_list.device) if out is None else out
+    out = _empty((n, w.rows), torch.int32, expert_list.device, stream) if out is None else out
     _check(lib().iqk_floor(ctypes.byref(w.c), expert_list.data_ptr(), n, out.data_ptr(), _stream(stream)),
            "iqk_floor")
     return out
@@ -497,9 +510,9 @@ def iqk_moe_topk(logits, topk: int, score: str = "softmax", bias=None, groups: i
         raise ValueError(f"logits must be float32 or bfloat16 on a CUDA device and score one of {sorted(_SCORES)}, "
                          f"got {dt} on {logits.device} and {score!r}")
     if ids is None:
-        ids = _empty(shape, torch.int32, logits.device)
+        ids = _empty(shape, torch.int32, logits.device, stream)
     if p is None:
-        p = _empty(shape, torch.float32, logits.device)
+        p = _empty(shape, torch.float32, logits.device, stream)
     if not (ids.dtype is torch.int32 and p.dtype is torch.float32 and ids.get_device() == p.get_device() == at
             and ids.shape == p.shape == shape and ids.is_contiguous() and p.is_contiguous()):
         _explain(at, (ids, shape, torch.int32, "ids"), (p, shape, torch.float32, "p"))
@@ -531,9 +544,9 @@ def iqk_fp8_quantize(x, q=None, s=None, stream=None):
     if at < 0 or x.dtype is not torch.bfloat16:
         raise ValueError(f"x must be bfloat16 on a CUDA device, got {x.dtype} on {x.device}")
     if q is None:
-        q = _empty(shape, f8, x.device)
+        q = _empty(shape, f8, x.device, stream)
     if s is None:
-        s = _empty(sshape, f32, x.device)
+        s = _empty(sshape, f32, x.device, stream)
     if not (q.dtype is f8 and s.dtype is f32 and q.get_device() == s.get_device() == at and q.shape == shape
             and s.shape == sshape and q.is_contiguous() and s.is_contiguous()):
         _explain(at, (q, shape, f8, "q"), (s, sshape, f32, "s"))
@@ -563,7 +576,7 @@ def iqk_fp8_linear(wq, ws, xq, xs, add=None, y=None, dtype=None, stream=None):
         raise ValueError("y must be bfloat16 or float32")
     shape, wsshape, xshape, xsshape = (T, rows), ((rows + 127) >> 7, nkb), (T, cols), (T, nkb)
     if y is None:
-        y = _empty(shape, dtype, wq.device)
+        y = _empty(shape, dtype, wq.device, stream)
     if not (at >= 0 and wq.dtype is f8 and xq.dtype is f8 and ws.dtype is f32 and xs.dtype is f32 and y.dtype is dtype
             and ws.get_device() == xq.get_device() == xs.get_device() == y.get_device() == at
             and ws.shape == wsshape and xq.shape == xshape and xs.shape == xsshape and y.shape == shape
@@ -596,9 +609,9 @@ def iqk_fp8_gate_up(gate_q, gate_s, up_q, up_s, xq, xs, q=None, s=None, stream=N
     T, nkb, nhb = xq.shape[0], (cols + 127) >> 7, (inter + 127) >> 7
     sshape, xshape, xsshape, qshape, hshape = (nhb, nkb), (T, cols), (T, nkb), (T, inter), (T, nhb)
     if q is None:
-        q = _empty(qshape, f8, gate_q.device)
+        q = _empty(qshape, f8, gate_q.device, stream)
     if s is None:
-        s = _empty(hshape, f32, gate_q.device)
+        s = _empty(hshape, f32, gate_q.device, stream)
     if not (at >= 0 and gate_q.dtype is f8 and up_q.dtype is f8 and xq.dtype is f8 and q.dtype is f8
             and gate_s.dtype is f32 and up_s.dtype is f32 and xs.dtype is f32 and s.dtype is f32
             and gate_s.get_device() == up_q.get_device() == up_s.get_device() == xq.get_device() == xs.get_device()
@@ -688,10 +701,11 @@ class IqkSwitchLinear:
         if indices.shape[:-1] != x.shape[:-1]:
             raise ValueError("indices must be [..., k] over the same leading shape as x")
         lead, k = tuple(x.shape[:-1]), indices.shape[-1]
-        xt = x.reshape(-1, self.in_features).contiguous()
-        ids = indices.reshape(-1, k).to(torch.int32).contiguous()
-        T = xt.shape[0]
         st = torch.cuda.current_stream(x.device) if stream is None else stream
+        with torch.cuda.stream(st):  # copies, where they are needed, too
+            xt = x.reshape(-1, self.in_features).contiguous()
+            ids = indices.reshape(-1, k).to(torch.int32).contiguous()
+        T = xt.shape[0]
         key = (mode, T, k, st.cuda_stream)
         ws = self._ws.get(key)
         if ws is None:
@@ -699,7 +713,7 @@ class IqkSwitchLinear:
                                                      self.in_features)
             if need == 0:
                 raise RuntimeError(f"IqkSwitchLinear: mode {mode} cannot take {T} tokens x {k} slots")
-            ws = self._ws[key] = workspace(need, x.device)
+            ws = self._ws[key] = workspace(need, x.device, st)
         self._last_ws = (ws, st)
         y = iqk_switch_linear(self.weights, self.values, xt, ids, mode=mode, ws=ws, stream=st)
         return y.reshape(*lead, k, self.out_features)

@@ -166,6 +166,38 @@ def test_two_streams_and_two_graphs_at_once(T):
             assert all(torch.equal(a, b) for a, b in zip(o, alone[i]))
 
 
+def pool_of(t):
+    """The stream whose pool of the caching allocator a tensor's memory is from."""
+    at = t.data_ptr()
+    return next(s["stream"] for s in torch.cuda.memory_snapshot() if s["address"] <= at < s["address"] + s["total_size"])
+
+
+def test_memory_of_a_call_is_from_its_streams_pool():
+    """What a call on a given stream allocates is ordered by that stream: a
+    block of the current stream's pool may still be written to there."""
+    T = 40
+    wq, ws = F.operand(1, 528, 512, 128)
+    xq, xs = F.operand(2, T, 512, 1)
+    x, lg = F.activations(3, T, 512), R.logits(4, T, 96)
+    rng = S.rng_for(3)
+    w = B.Weights.from_host(S.random_streams(rng, "iq2_ks", 4, 512, 512))
+    values = S.value_table("dyadic", 8)
+    ids = torch.zeros((T, 2), dtype=torch.int32, device="cuda")
+    st = torch.cuda.Stream()
+    calls = [lambda **k: B.iqk_moe_topk(lg, 5, **k), lambda **k: B.iqk_fp8_quantize(x, **k),
+             lambda **k: [B.iqk_fp8_linear(wq, ws, xq, xs, **k)], lambda **k: B.iqk_fp8_gate_up(wq, ws, wq, ws, xq, xs, **k),
+             lambda **k: [B.iqk_dequant(w, 1, values, **k)], lambda **k: [B.iqk_gemv(w, 1, values, x[:2], **k)],
+             lambda **k: [B.iqk_switch_linear(w, values, x, ids, **k)], lambda **k: B.iqk_moe_route(ids, 4, **k)[:3]]
+    for call in calls:
+        want = call()
+        torch.cuda.synchronize()
+        got = call(stream=st)
+        assert all(pool_of(t) == st.cuda_stream for t in got)
+        assert all(pool_of(t) != st.cuda_stream for t in want)
+        st.synchronize()
+        assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(got, want))
+
+
 @pytest.mark.parametrize("T", [1, 9, 300])
 def test_weights_written_just_before_the_call_are_read(T):
     """Stream order holds for weights and scales, too."""
