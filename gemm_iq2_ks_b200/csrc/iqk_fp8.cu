@@ -561,6 +561,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   constexpr int SB = kGemmStageBytes(BN, PAIR), ST = kGemmRing(BN, PAIR) / SB, NC = BN / 4;
   constexpr int NBUF = 512 / BN;  // accumulators in tensor memory
   constexpr int NB = GU ? 128 : BN;  // output columns of a tile
+  static_assert(BN == (GU || PAIR ? 256 : 128), "the forms that launch_fp8_product takes");
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   uint8_t* staging = smem + kGemmRing(BN, PAIR);
@@ -641,7 +642,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
               mbar_arrive_expect_tx(&full[s], SB);
               tma_load_2d(a, &mx, k, t0, &full[s]);
               tma_load_2d(w, &m0, k, n0, &full[s]);
-              if (BN == 256) tma_load_2d(w + 128 * kFp8Block, &m1, k, GU ? n0 : n0 + 128, &full[s]);
+              if (GU) tma_load_2d(w + 128 * kFp8Block, &m1, k, n0, &full[s]);
             }
           }
           __syncwarp();
