@@ -11,6 +11,7 @@ import concurrent.futures as cf
 import glob
 import hashlib
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -24,7 +25,12 @@ LIB = os.path.join(OUT_DIR, "libiqk.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
-         "-Xptxas", "-warn-spills", "-I", INCLUDE, "-I", CSRC]
+         "-Xptxas", "-warn-spills,-v", "-I", INCLUDE, "-I", CSRC]
+
+# Registers a thread that a kernel has to be launched with: its warps hand
+# registers on among themselves (setmaxnreg), and the shares add up to exactly
+# this. With fewer the library refuses the call.
+REGISTERS = {"k_fp8_gemm": 96}
 
 
 def _nvcc() -> str:
@@ -53,6 +59,14 @@ def _stamp() -> str:
     return h.hexdigest()
 
 
+def check_registers(report: str) -> None:
+    """Raise where ptxas reports another register count for a kernel of REGISTERS."""
+    for name, used in re.findall(r"Compiling entry function '(\w+)'.*?Used (\d+) registers", report, re.S):
+        for kernel, want in REGISTERS.items():
+            if kernel in name and int(used) != want:
+                raise RuntimeError(f"{name} was compiled to {used} registers a thread, its register split needs {want}")
+
+
 def up_to_date() -> bool:
     stamp = os.path.join(OUT_DIR, "stamp")
     if not (os.path.exists(LIB) and os.path.exists(stamp)):
@@ -71,11 +85,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
     def compile_one(src):
         obj = os.path.join(OUT_DIR, os.path.basename(src)[:-3] + ".o")
         cmd = [nvcc] + ARCH + FLAGS + ["-c", src, "-o", obj]
-        if verbose:
-            cmd += ["-Xptxas", "-v"]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"nvcc failed for {src}:\n{r.stderr}")
+        check_registers(r.stdout + r.stderr)
         return obj, r.stderr
 
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 4)) as ex:
