@@ -58,7 +58,8 @@ __device__ __forceinline__ float quick_inverse(float m) {
   return r * 1.75f;
 }
 // m / 448 rounded to nearest for a bfloat16 m: product with the rounded
-// reciprocal and one correction (exact for all 128 mantissas).
+// reciprocal and one correction by the fused remainder (Markstein 1990; exact
+// for all 128 mantissas).
 __device__ __forceinline__ float over_448(float m) {
   constexpr float r = 1.0f / 448.0f;
   const float q = m * r;
@@ -196,16 +197,18 @@ __device__ __forceinline__ float magnitude(float h) {  // infinity for what is n
 // shared memory for its weights (128 x 256 x 32 alone took 196 cycles, of 128
 // that the tensor cores need).
 //
-// What bounds it is the hand-over of the accumulators: a step's sums have to
-// leave tensor memory before the MMAs of the second next step, 64 KB at a time
-// for each CTA. What counted there, measured at 8192 x 4096 x 4096: the token
-// scales go through shared memory (each row of a warp's direct load is a line
-// of its own: +12%), on the barrier that the step waits for anyway (a barrier
-// of their own: +20%), arrivals and waits have CTA scope (what they order is
+// What bounds it is the hand-over of the accumulators: a step's sums (128 rows x
+// 256 columns, 128 KB for each CTA of a pair) have to leave tensor memory before
+// the MMAs of the second next step; a step takes 940 cycles, its MMAs 512. What
+// counted there, measured at 8192 x 4096 x 4096: the token scales go through
+// shared memory (each row of a warp's direct load is a line of its own: +12%),
+// on the barrier that the step waits for anyway (a barrier of their own: +20%),
+// the larger factors of far scales are read beside them (a flag read ahead of
+// the loads instead: +8%), arrivals and waits have CTA scope (what they order is
 // tensor memory, by its own fences; cluster scope took twice the time), and no
-// register of the loop is spilled (+10 to 20% for a few bytes). 131 us on
-// operands of small codes (2.10 PFLOP/s); quantised normal data takes 153 to
-// 160 us at the same instructions, the card's power limit slows it down.
+// register of the loop is spilled (+10 to 20% for a few bytes). 125 us on
+// operands of small codes (2.20 PFLOP/s); quantised normal data takes 132 to
+// 152 us at the same instructions, the longer it runs, by the card's power limit.
 constexpr int kBM = 128;
 constexpr int kEpiWarps = 16, kTmaWarp = 16, kMmaWarp = 17, kScaleWarp = 18;  // and 19
 constexpr int kGemmThreads = 20 * 32;
@@ -467,7 +470,7 @@ constexpr int kMaxSplit = 8;  // CTAs of a cluster
 // CTAs of the accumulators at `src` in each one's shared memory, in rank order,
 // and what becomes of it. Gate_up: 128 gate columns, then their up columns.
 // WIDE: all loads on their way before the first is used, where there are
-// registers for it (gate_up of 1 token 7.1 to 6.4 us).
+// registers for it (0.7 us less for gate_up of 1 token).
 template <int V, bool GU, bool WIDE>
 __device__ __forceinline__ void finish_row(const Fp8Args& A, const float* src, int split, int64_t t, int n0, int lane) {
   float4 v[V];
@@ -931,9 +934,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 // token rows would be mostly padding. Thread = weight row; the token scales,
 // times the block's, come from a table that each warp writes for each step.
 // A latency chain bounds it (start, first copies, a few steps, the exchange in
-// the cluster): 4096 x 4096 takes 5.0 us for 1 token and 6.3 us for 32 (3.4 and
-// 2.7 TB/s), where a 64-token form took 8.2 us, no less than the tiles above,
-// and a stream over the weights with mma.sync 5.1 us for 1 and 10.9 for 16.
+// the cluster): 4096 x 4096 takes 4.8 us for 1 token and 6.3 us for 32 (3.5 and
+// 2.7 TB/s, operands in L2; 5.8 and 7.3 us over three sets of them), where a
+// 64-token form took 8.2 us, no less than the tiles above, and a stream over
+// the weights with mma.sync 5.1 us for 1 and 10.9 for 16.
 constexpr int kSkinnyThreads = 6 * 32;
 constexpr int kSkinnyMaxT = 32;
 constexpr int kSkStage(bool gu, int TN) { return ((gu ? 256 : 128) + TN) * kFp8Block; }
@@ -942,6 +946,9 @@ constexpr int kSkBufs = 4;  // accumulators in tensor memory: at most 256 column
 constexpr int kSkRing(bool gu, int TN) { return kSkStages(gu) * kSkStage(gu, TN); }
 constexpr size_t kSkSmem(bool gu, int TN) { return kSkRing(gu, TN) + 2 * (4 * 2 * kSkinnyMaxT * 4) + 256 + 1024; }
 static_assert(kSkRing(true, 32) >= 32 * 256 * 4 && kSkRing(false, 32) >= 32 * 128 * 4, "accumulators");
+// Two CTAs fit on an SM by shared memory, registers and tensor memory; how many
+// clusters do is asked of the runtime (pick_split: 16 tiles of gate_up get
+// clusters of 6, 96 CTAs).
 static_assert(kSkSmem(true, 32) <= 113 * 1024 && kSkSmem(false, 32) <= 113 * 1024, "two CTAs on an SM");
 
 template <bool GU, int TN>
@@ -1172,7 +1179,9 @@ int make_e4m3_map(CUtensorMap* map, const uint8_t* base, int rows, int cols, int
 
 // CTAs that a tile's blocks are split over: the least time by the steps in a
 // row, times the waves that the clusters need (a cluster lives inside one GPC,
-// so 8 CTAs of one per SM fit 15 times, not 18, into 148 SMs).
+// so 8 CTAs of one per SM fit 15 times, not 18, into 148 SMs). The two constants
+// are estimates from a call's parts (start-up 0.7 us and first copies 0.9 us,
+// two cluster barriers and the exchange, against 0.3 us a step), not fitted.
 constexpr int kTileSteps = 6;   // start, drain and stores of a tile, in steps
 constexpr int kSplitSteps = 6;  // the exchange between the CTAs of a cluster
 
@@ -1288,9 +1297,13 @@ int launch_fp8_product(Fp8Args a, bool gate_up, cudaStream_t st, int num_sms) {
     if (gate_up) return a.T <= 16 ? launch_skinny<true, 16>(a, num_sms, st) : launch_skinny<true, 32>(a, num_sms, st);
     return a.T <= 16 ? launch_skinny<false, 16>(a, num_sms, st) : launch_skinny<false, 32>(a, num_sms, st);
   }
-  // Pairs of CTAs where their tiles occupy a third of the SMs or more: at 4096 x
-  // 4096 weights 1024 tokens (64 tiles) take 22.8 us by pairs and 27.3 us by
-  // single CTAs, 512 tokens (32 tiles) 21.9 and 15.5 us.
+  // Pairs of CTAs where their tiles occupy a third of the SMs or more. Pairs and
+  // single CTAs at 4096 x 4096 weights: 512 tokens (32 tiles) 19.1 and 13.3 us,
+  // 768 (48) 20.1 and 23.6, 1024 (64) 20.5 and 23.9; 4096 tokens of 1024 x 2048
+  // (64) 13.5 and 14.5; gate_up of 2048 x 4096: 512 tokens (32) 20.1 and 17.3 us,
+  // 768 (48) and 1024 (64) alike within 3%. The border is on the wrong side for
+  // 640 to 768 tokens of the first (15%) and where rows of tokens are mostly
+  // padding (300 tokens of 16384 x 1024: 16.0 and 13.0 us).
   const int cols = gate_up ? 128 : 256;
   const int64_t pairs = (int64_t)((a.T + 255) / 256) * ((a.rows + cols - 1) / cols);
   if (pairs * 3 >= num_sms)

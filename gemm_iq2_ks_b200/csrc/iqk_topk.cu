@@ -14,12 +14,15 @@
 // float32's error (or alike in the bits that the index leaves), the
 // candidates are ordered anew from whole values, in float64 if they are
 // scores, so the selection is that of the float64 scores for every row and the
-// cheap arithmetic serves nearly all of them. Instructions bound it: about 250
-// for a row of 256, most of them on the half-rate integer pipe. 65536 rows of
-// bf16 logits take 22 us (1.7 TB/s; with one maximum for the value and one for
-// the index over whole keys 51 us), 2048 rows of grouped sigmoid routing 9.6 us,
-// one row 1.8 us. Warps that loop over rows with the next one fetched ahead were
-// slower (24.7 and 11.4 us).
+// cheap arithmetic serves nearly all of them. Instructions bound it: 280 for a
+// plain row of 256 bf16 logits, most of them on the half-rate integer pipe.
+// 65536 such rows take 22 us (1.7 TB/s; with one maximum for the value and one
+// for the index over whole keys 51 us; of float32 logits 30 us, 2.3 TB/s), one
+// row 1.8 us. 2048 rows of grouped sigmoid routing (1170 instructions a row)
+// take 7 to 8 us, and 13.5 to 14.3 us where the groups of some row are in doubt
+// and one warp orders the whole row in float64 (a third of random inputs). Warps
+// that loop over rows with the next one fetched ahead were slower (24.7 and
+// 11.4 us).
 #include <algorithm>
 
 #include "iqk_device.cuh"

@@ -490,9 +490,12 @@ typedef enum { IQK_SOFTMAX = 0, IQK_SIGMOID = 1 } iqk_score;
  *   ids:    device int32 [T][topk]: the open experts of largest selection value
  *           in descending order, ties to the lowest index
  *   p:      device float32 [T][topk]: scale * s, or with renorm != 0
- *           scale * s / (sum of the selected s), float32 arithmetic; the ratio
- *           is formed from the logits, so it also holds where the scores
- *           themselves lie below float32's range
+ *           scale * s / (sum of the selected s); the ratio is formed from the
+ *           logits, so it also holds where the scores themselves lie below
+ *           float32's range. float32 arithmetic, with the hardware's fast
+ *           exponential in the softmax's sum and its fast division: within
+ *           (d + experts / 32 + 64) 2^-24 of itself, d the spread of the row's
+ *           finite logits, above 2^-126 scale
  * A logit of -inf or NaN, or a bias of -inf or NaN, masks the expert: it comes
  * behind every other open expert and its p is 0 (a row masked throughout gets
  * valid ids and p = 0 everywhere). The softmax is over the logits that are not
