@@ -1181,7 +1181,7 @@ int make_e4m3_map(CUtensorMap* map, const uint8_t* base, int rows, int cols, int
 // row, times the waves that the clusters need (a cluster lives inside one GPC,
 // so 8 CTAs of one per SM fit 15 times, not 18, into 148 SMs). The two constants
 // are estimates from a call's parts (start-up 0.7 us and first copies 0.9 us,
-// two cluster barriers and the exchange, against 0.3 us a step), not fitted.
+// two cluster barriers and the exchange, against 0.35 us a step), not fitted.
 constexpr int kTileSteps = 6;   // start, drain and stores of a tile, in steps
 constexpr int kSplitSteps = 6;  // the exchange between the CTAs of a cluster
 
